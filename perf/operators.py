@@ -159,7 +159,7 @@ def prepare(case, seed):
     if op in ("plan", "balance"):
         T, E, k = case["tokens"], case["experts"], case["top_k"]
         logits, s["idx"], s["valid"] = _routing(case, g)
-        s["counts"] = torch.empty(E + 1, dtype=torch.int32, device="cuda")
+        s["counts"] = torch.empty(E if op == "plan" else E + 1, dtype=torch.int32, device="cuda")
         if op == "plan":
             s["offsets"] = torch.empty(E + 1, dtype=torch.int32, device="cuda")
             s["rows"] = torch.empty(T * k, dtype=torch.int32, device="cuda")
@@ -224,8 +224,7 @@ def _plan(s):
     rows = torch.where(sorted_key < E, order // k, -1)
     slots = torch.empty_like(flat).scatter_(0, order, torch.arange(flat.numel(), device=flat.device))
     slots = torch.where(used, slots, -1).view(-1, k)
-    counts[E] = used.view(-1, k).any(1).sum()  # tokens with a choice
-    return {"counts": counts.int(), "offsets": offsets, "rows": rows.int(), "slots": slots.int()}
+    return {"counts": counts[:E].int(), "offsets": offsets, "rows": rows.int(), "slots": slots.int()}
 
 
 def _balance(s):
