@@ -1,0 +1,488 @@
+// The router's balance loss and its gradient.
+//
+// Over the n tokens that count (all of them, or those `valid` marks), with
+// p_te = softmax_e(l_t) and c_e the number of their choices that name expert e:
+//
+//   P_e  = 1/n sum_t p_te,   f_e = E c_e / (k n),   loss = sum_e f_e P_e
+//   d loss / d l_te = p_te (f_e - sum_j f_j p_tj) / n
+//
+// (f comes from the choices, which have no gradient.)  The loss is 1 when
+// choices and probabilities are uniform.
+//
+// Forward: a warp takes one row of logits at a time, holds it in registers
+// (E <= 1024, at most 32 values a lane) for maximum, exponentials and sum, and
+// adds the probabilities to its own columns' registers; choices go to a
+// shared-memory histogram.  A CTA's column sums meet the other CTAs' in a fixed
+// order: within one thread-block cluster through distributed shared memory
+// when at most 8 CTAs have work (one launch), else through the workspace in a
+// second launch.  No floating-point atomics: results are reproducible bit for
+// bit.  All sums are fp32.
+// Backward: the row is read again and its softmax recomputed, which costs a
+// read of the logits but no saved tensor as large as they are.
+// Both are bound by the logits' bytes at prefill sizes and by launch latency
+// at decode sizes.
+#include <algorithm>
+
+#include "op_common.cuh"
+
+namespace moe {
+namespace {
+
+using namespace op;
+
+constexpr int kBalWarps = 16, kBalThreads = 32 * kBalWarps;
+constexpr int kBalCluster = 8;      // CTAs of the cluster that adds the column sums
+constexpr int kBalMaxCtas = 148;    // CTAs with partial sums in the workspace
+constexpr int kBalRowsPerWarp = 2;  // below this many rows a warp, fewer CTAs
+
+// A lane's values of a row: NV of them, V consecutive at a time (16 bytes, or
+// one where rows are not 16-byte aligned); value (i, j) is column
+// (i * 32 + lane) * V + j.
+template <class T, int V>
+struct RowVec;
+template <>
+struct RowVec<float, 4> {
+    static __device__ __forceinline__ void load(const float *p, float (&v)[4])
+    {
+        const float4 r = __ldg(reinterpret_cast<const float4 *>(p));
+        v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w;
+    }
+    static __device__ __forceinline__ void store(float *p, const float (&v)[4])
+    {
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+};
+template <>
+struct RowVec<__nv_bfloat16, 8> {
+    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float (&v)[8])
+    {
+        const uint4 r = __ldg(reinterpret_cast<const uint4 *>(p));
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[8])
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+template <>
+struct RowVec<float, 1> {
+    static __device__ __forceinline__ void load(const float *p, float (&v)[1]) { v[0] = __ldg(p); }
+    static __device__ __forceinline__ void store(float *p, const float (&v)[1]) { *p = v[0]; }
+};
+template <>
+struct RowVec<__nv_bfloat16, 1> {
+    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float (&v)[1]) { v[0] = __bfloat162float(*p); }
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[1]) { *p = __float2bfloat16_rn(v[0]); }
+};
+
+template <class T, int NV, int V>
+__device__ __forceinline__ void load_row(const T *row, int E, int lane, float (&v)[NV])
+{
+#pragma unroll
+    for (int i = 0; i < NV / V; ++i) {
+        const int c = (i * 32 + lane) * V;
+        float u[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) u[j] = -INFINITY;
+        if (c < E) RowVec<T, V>::load(row + c, u);  // V > 1 only where E is a multiple of V
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[i * V + j] = u[j];
+    }
+}
+
+// v becomes the row's probabilities.  A row of only -inf has none (all zero); a
+// NaN or +inf makes the whole row NaN, as the definition does.
+template <int NV>
+__device__ __forceinline__ void row_softmax(float (&v)[NV])
+{
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) m = fmaxf(m, v[i]);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    // fmaxf passes over NaN: those come back through exp(NaN - m) below; with
+    // m = -inf subtract 0 so that an empty row gives exp(-inf) = 0
+    const float shift = m == -INFINITY ? 0.f : m;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        v[i] = expf(v[i] - shift);
+        s += v[i];
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    const float inv = s == 0.f ? 0.f : 1.f / s;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] *= inv;
+}
+
+struct BalanceArgs {
+    const void *logits;
+    const int32_t *idx;
+    const uint8_t *valid;
+    int T, E, k, ctas;
+    float *psum;      // [ctas][E] workspace
+    int32_t *pcount;  // [ctas][E]
+    int32_t *pvalid;  // [ctas]
+    int32_t *counts;
+    float *prob_mean, *loss;
+};
+
+// Column sums, counts and P, f, loss from the partial sums of `ctas` CTAs: the
+// cluster's CTA r owns columns [r * cols, (r + 1) * cols).  Partials lie in
+// the workspace, or in the cluster's shared memory (DSMEM).
+template <bool DSMEM>
+__device__ void balance_reduce(const BalanceArgs &a, const float *s_sum, const int32_t *s_cnt, const int32_t *s_valid)
+{
+    __shared__ float red_p[kBalWarps][32];
+    __shared__ int32_t red_c[kBalWarps][32];
+    __shared__ int n_valid;
+    __shared__ float loss_part;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned rank = cluster_rank(), ranks = cluster_size();
+    const int cols = (int)((a.E + ranks - 1) / ranks);
+    const int c0 = (int)rank * cols, c1 = min(a.E, c0 + cols);
+    const uint32_t sum_at = DSMEM ? static_cast<uint32_t>(__cvta_generic_to_shared(s_sum)) : 0;
+    const uint32_t cnt_at = DSMEM ? static_cast<uint32_t>(__cvta_generic_to_shared(s_cnt)) : 0;
+    const uint32_t valid_at = DSMEM ? static_cast<uint32_t>(__cvta_generic_to_shared(s_valid)) : 0;
+
+    if (warp == 0) {
+        int n = 0;
+        for (int g = lane; g < a.ctas; g += 32) n += DSMEM ? (int)cluster_ld_u32(cluster_map(valid_at, g)) : a.pvalid[g];
+#pragma unroll
+        for (int d = 16; d; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
+        if (lane == 0) n_valid = n;
+    }
+    __syncthreads();
+    const int n = n_valid;
+    const float inv_n = 1.f / (float)max(n, 1);
+    const float to_share = (float)((double)a.E / ((double)a.k * (double)max(n, 1)));
+    float loss = 0.f;
+    for (int cb = c0; cb < c1; cb += 32) {
+        const int c = cb + lane;
+        float p = 0.f;
+        int cnt = 0;
+        if (c < c1) {
+            for (int g = warp; g < a.ctas; g += kBalWarps) {
+                if (DSMEM) {
+                    p += cluster_ld_f32(cluster_map(sum_at, g) + 4 * c);
+                    cnt += (int)cluster_ld_u32(cluster_map(cnt_at, g) + 4 * c);
+                } else {
+                    p += a.psum[(size_t)g * a.E + c];
+                    cnt += a.pcount[(size_t)g * a.E + c];
+                }
+            }
+        }
+        red_p[warp][lane] = p;
+        red_c[warp][lane] = cnt;
+        __syncthreads();
+        if (warp == 0 && c < c1) {
+            for (int w = 1; w < kBalWarps; ++w) {
+                p += red_p[w][lane];
+                cnt += red_c[w][lane];
+            }
+            p *= inv_n;
+            a.prob_mean[c] = p;
+            a.counts[c] = cnt;
+            loss += (float)cnt * to_share * p;
+        }
+        __syncthreads();
+    }
+    if (warp == 0) {
+#pragma unroll
+        for (int d = 16; d; d >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, d);
+        if (lane == 0) loss_part = loss;
+    }
+    if (ranks > 1) cluster_sync();
+    else __syncthreads();
+    if (rank == 0 && threadIdx.x == 0) {
+        const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(&loss_part));
+        float l = 0.f;
+        for (unsigned r = 0; r < ranks; ++r) l += ranks > 1 ? cluster_ld_f32(cluster_map(at, r)) : loss_part;
+        *a.loss = l;
+        a.counts[a.E] = n;
+    }
+    if (ranks > 1) cluster_sync();  // the other CTAs' shared memory is read until here
+}
+
+// CLUSTER: the grid is one cluster and finishes the loss itself.
+template <class T, int NV, int V, bool CLUSTER>
+__global__ void __launch_bounds__(kBalThreads, 1) balance_forward_kernel(const BalanceArgs a)
+{
+    extern __shared__ float bal_smem[];
+    float *warp_cols = bal_smem;                                   // [kBalWarps][E]
+    float *cta_sum = warp_cols + kBalWarps * a.E;                  // [E]
+    int32_t *hist = reinterpret_cast<int32_t *>(cta_sum + a.E);    // [E]
+    __shared__ int32_t cta_valid;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const T *logits = static_cast<const T *>(a.logits);
+    for (int e = threadIdx.x; e < a.E; e += kBalThreads) hist[e] = 0;
+    if (threadIdx.x == 0) cta_valid = 0;
+    __syncthreads();
+
+    float acc[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) acc[i] = 0.f;
+    int n_valid = 0;
+    const int step = gridDim.x * kBalWarps;
+    int t = blockIdx.x * kBalWarps + warp;
+    float next[NV];
+    if (t < a.T) load_row<T, NV, V>(logits + (size_t)t * a.E, a.E, lane, next);
+    for (; t < a.T; t += step) {
+        float v[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] = next[i];
+        if (t + step < a.T) load_row<T, NV, V>(logits + (size_t)(t + step) * a.E, a.E, lane, next);
+        if (a.valid && !a.valid[t]) continue;
+        ++n_valid;
+        for (int j = lane; j < a.k; j += 32) {
+            const int e = __ldg(a.idx + (size_t)t * a.k + j);
+            if ((unsigned)e < (unsigned)a.E) atomicAdd(&hist[e], 1);
+        }
+        row_softmax<NV>(v);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) acc[i] += v[i];
+    }
+#pragma unroll
+    for (int i = 0; i < NV / V; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = (i * 32 + lane) * V + j;
+            if (c < a.E) warp_cols[warp * a.E + c] = acc[i * V + j];
+        }
+    if (lane == 0 && n_valid) atomicAdd(&cta_valid, n_valid);
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += kBalThreads) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kBalWarps; ++w) s += warp_cols[w * a.E + e];
+        if (CLUSTER) {
+            cta_sum[e] = s;
+        } else {
+            a.psum[(size_t)blockIdx.x * a.E + e] = s;
+            a.pcount[(size_t)blockIdx.x * a.E + e] = hist[e];
+        }
+    }
+    if (CLUSTER) {
+        if (cluster_size() > 1) cluster_sync();
+        else __syncthreads();
+        balance_reduce<true>(a, cta_sum, hist, &cta_valid);
+    } else {
+        if (threadIdx.x == 0) a.pvalid[blockIdx.x] = cta_valid;
+        dependents_launch();
+    }
+}
+
+__global__ void __launch_bounds__(kBalThreads, 1) balance_reduce_kernel(const BalanceArgs a)
+{
+    dependents_wait();
+    balance_reduce<false>(a, nullptr, nullptr, nullptr);
+}
+
+constexpr int kBwdWarps = 8, kBwdThreads = 32 * kBwdWarps;
+
+template <class T, int NV, int V>
+__global__ void __launch_bounds__(kBwdThreads)
+    balance_backward_kernel(const T *__restrict__ logits, const int32_t *__restrict__ counts,
+                            const uint8_t *__restrict__ valid, const float *__restrict__ dloss, int tokens, int E, int k,
+                            T *__restrict__ dlogits)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const double n = (double)max(__ldg(counts + E), 1);
+    const float to_share = (float)((double)E / ((double)k * n));
+    const float scale = __ldg(dloss) / (float)n;
+    float f[NV];
+#pragma unroll
+    for (int i = 0; i < NV / V; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = (i * 32 + lane) * V + j;
+            f[i * V + j] = c < E ? (float)__ldg(counts + c) * to_share : 0.f;
+        }
+    for (int t = blockIdx.x * kBwdWarps + warp; t < tokens; t += gridDim.x * kBwdWarps) {
+        float v[NV];
+        const bool counted = !valid || valid[t];
+        if (counted) {
+            load_row<T, NV, V>(logits + (size_t)t * E, E, lane, v);
+            row_softmax<NV>(v);
+            float dot = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) dot += f[i] * v[i];
+#pragma unroll
+            for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) v[i] = scale * v[i] * (f[i] - dot);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) v[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < NV / V; ++i) {
+            const int c = (i * 32 + lane) * V;
+            float u[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) u[j] = v[i * V + j];
+            if (c < E) RowVec<T, V>::store(dlogits + (size_t)t * E + c, u);
+        }
+    }
+}
+
+size_t balance_smem(int E) { return sizeof(float) * (size_t)E * (kBalWarps + 2); }
+
+typedef void (*ForwardKernel)(const BalanceArgs);
+
+template <class T, int NV, int V>
+ForwardKernel forward_of(bool cluster)
+{
+    return cluster ? balance_forward_kernel<T, NV, V, true> : balance_forward_kernel<T, NV, V, false>;
+}
+
+// Rows are read 16 bytes at a time where every row starts on a 16-byte
+// boundary, else value by value.
+template <class T, int W>
+ForwardKernel forward_pick(int E, bool wide, bool cluster)
+{
+    if (wide) {
+        if (E <= 256) return forward_of<T, 8, W>(cluster);
+        return E <= 512 ? forward_of<T, 16, W>(cluster) : forward_of<T, 32, W>(cluster);
+    }
+    if (E <= 256) return forward_of<T, 8, 1>(cluster);
+    return E <= 512 ? forward_of<T, 16, 1>(cluster) : forward_of<T, 32, 1>(cluster);
+}
+
+template <class T, int W>
+auto backward_pick(int E, bool wide) -> decltype(&balance_backward_kernel<T, 8, W>)
+{
+    if (wide) {
+        if (E <= 256) return balance_backward_kernel<T, 8, W>;
+        return E <= 512 ? balance_backward_kernel<T, 16, W> : balance_backward_kernel<T, 32, W>;
+    }
+    if (E <= 256) return balance_backward_kernel<T, 8, 1>;
+    return E <= 512 ? balance_backward_kernel<T, 16, 1> : balance_backward_kernel<T, 32, 1>;
+}
+
+bool wide_rows(const void *p, const void *q, moe_dtype dt, int E)
+{
+    return aligned(p, 16) && aligned(q, 16) && E % (dt == MOE_DT_BF16 ? 8 : 4) == 0;
+}
+
+int forward_ctas(int T)
+{
+    const int n = std::max(1, std::min(kBalMaxCtas, ceil_div(T, kBalWarps * kBalRowsPerWarp)));
+    return n > kBalCluster ? n : n > 4 ? 8 : n > 2 ? 4 : n;  // a cluster of 1, 2, 4 or 8
+}
+
+PerDevice g_balance;
+
+cudaError_t balance_prepare()
+{
+    for (int E : {256, 512, 1024})
+        for (int wide = 0; wide < 2; ++wide)
+            for (int cluster = 0; cluster < 2; ++cluster)
+                for (int bf = 0; bf < 2; ++bf) {
+                    ForwardKernel f = bf ? forward_pick<__nv_bfloat16, 8>(E, wide, cluster)
+                                         : forward_pick<float, 4>(E, wide, cluster);
+                    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                               (int)balance_smem(kMaxExperts));
+                    if (e != cudaSuccess) return e;
+                }
+    return cudaSuccess;
+}
+
+bool balance_sizes_ok(moe_dtype dt, int T, int E, int k)
+{
+    return (dt == MOE_DT_F32 || dt == MOE_DT_BF16) && T >= 0 && T <= (1 << 30) && E >= 1 && E <= kMaxExperts && k >= 1 &&
+           k <= E;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t moe_balance_loss_workspace_bytes(int n_tokens, int n_experts)
+{
+    if (n_tokens <= 0 || n_experts < 1 || n_experts > kMaxExperts) return 0;
+    const int ctas = forward_ctas(n_tokens);
+    return ctas <= kBalCluster ? 0 : (size_t)ctas * n_experts * 8 + (size_t)ctas * 4;
+}
+
+extern "C" moe_status moe_balance_loss(const void *logits, moe_dtype dtype, const int32_t *idx, const uint8_t *valid,
+                                       int n_tokens, int n_experts, int top_k, float *loss, int32_t *counts,
+                                       float *prob_mean, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!balance_sizes_ok(dtype, n_tokens, n_experts, top_k)) return MOE_ERR_INVALID_ARG;
+    if (!loss || !counts || !prob_mean) return MOE_ERR_INVALID_ARG;
+    if (n_tokens && (!logits || !idx)) return MOE_ERR_INVALID_ARG;
+    if (!aligned(logits, dtype == MOE_DT_BF16 ? 2 : 4) || !aligned(idx, 4) || !aligned(loss, 4) ||
+        !aligned(counts, 4) || !aligned(prob_mean, 4))
+        return MOE_ERR_INVALID_ARG;
+    const size_t need = moe_balance_loss_workspace_bytes(n_tokens, n_experts);
+    if (need && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return MOE_ERR_INVALID_ARG;
+    int sms = 0;
+    const moe_status st = g_balance.get(&sms, balance_prepare);
+    if (st != MOE_OK) return st;
+    BalanceArgs a{};
+    a.logits = logits;
+    a.idx = idx;
+    a.valid = valid;
+    a.T = n_tokens;
+    a.E = n_experts;
+    a.k = top_k;
+    a.ctas = forward_ctas(n_tokens);
+    a.counts = counts;
+    a.prob_mean = prob_mean;
+    a.loss = loss;
+    const bool cluster = a.ctas <= kBalCluster;
+    if (!cluster) {
+        a.psum = static_cast<float *>(workspace);
+        a.pcount = reinterpret_cast<int32_t *>(a.psum + (size_t)a.ctas * n_experts);
+        a.pvalid = a.pcount + (size_t)a.ctas * n_experts;
+    }
+    const bool wide = wide_rows(logits, nullptr, dtype, n_experts);
+    ForwardKernel f = dtype == MOE_DT_BF16 ? forward_pick<__nv_bfloat16, 8>(n_experts, wide, cluster)
+                                           : forward_pick<float, 4>(n_experts, wide, cluster);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = launch(f, dim3(a.ctas), kBalThreads, balance_smem(n_experts), s, cluster ? a.ctas : 1, false, a);
+    if (e == cudaSuccess && !cluster)
+        e = launch(balance_reduce_kernel, dim3(kBalCluster), kBalThreads, 0, s, kBalCluster, true, a);
+    return launched(e);
+}
+
+extern "C" moe_status moe_balance_loss_backward(const void *logits, moe_dtype dtype, const int32_t *counts,
+                                                const uint8_t *valid, const float *dloss, int n_tokens, int n_experts,
+                                                int top_k, void *dlogits, void *stream)
+{
+    if (!balance_sizes_ok(dtype, n_tokens, n_experts, top_k)) return MOE_ERR_INVALID_ARG;
+    if (n_tokens == 0) return MOE_OK;
+    if (!logits || !counts || !dloss || !dlogits) return MOE_ERR_INVALID_ARG;
+    const unsigned size = dtype == MOE_DT_BF16 ? 2 : 4;
+    if (!aligned(logits, size) || !aligned(dlogits, size) || !aligned(counts, 4) || !aligned(dloss, 4))
+        return MOE_ERR_INVALID_ARG;
+    int sms = 0;
+    const moe_status st = g_balance.get(&sms, balance_prepare);
+    if (st != MOE_OK) return st;
+    const bool wide = wide_rows(logits, dlogits, dtype, n_experts);
+    const int grid = std::min(ceil_div(n_tokens, kBwdWarps), sms * 4);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (dtype == MOE_DT_BF16)
+        backward_pick<__nv_bfloat16, 8>(n_experts, wide)<<<grid, kBwdThreads, 0, s>>>(
+            static_cast<const __nv_bfloat16 *>(logits), counts, valid, dloss, n_tokens, n_experts, top_k,
+            static_cast<__nv_bfloat16 *>(dlogits));
+    else
+        backward_pick<float, 4>(n_experts, wide)<<<grid, kBwdThreads, 0, s>>>(
+            static_cast<const float *>(logits), counts, valid, dloss, n_tokens, n_experts, top_k,
+            static_cast<float *>(dlogits));
+    return launched(cudaGetLastError());
+}

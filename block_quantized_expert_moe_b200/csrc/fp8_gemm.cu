@@ -1,0 +1,525 @@
+// The E4M3 product with scales per block of 128, plain and per expert group:
+//
+//   out[r, n] = sum_b a_scale[b, r] * b_scale[g, n / 128, b]
+//                     * sum_{c in block b} a[r, c] * b[g, n, c]
+//
+// for the rows r of group g, [offsets[g], offsets[g + 1]) (the plain product
+// is one group of all rows).
+//
+// The weight rows are the M side of the tensor-core tile (128 of them, one
+// weight scale per tile and block), the token rows its N side, so a group of
+// any size fills the M side and pays for its own rows only (in steps of 16):
+// a decode batch reads every weight once, and a prefill chunk's ragged groups
+// waste at most 15 columns a tile.  A group with more rows than the widest
+// tile is cut into equal tiles.
+//
+// Both scales change every 128 columns, so the tensor core's sum covers one
+// block only (four 128 x N x 32 instructions into one of the tensor-memory
+// buffers) and the epilogue warps add scale * partial to fp32 registers while
+// the next block is multiplied: one FMA per 128 multiply-adds.  That split
+// also keeps the tensor core's accumulation short.
+//
+//   warps 0 .. E-1  epilogue: a thread owns one weight row (tensor-memory lane)
+//                   and the tile's columns (two warpgroups: half of them each)
+//   warp E          TMA producer of weight and token rows (128-byte swizzle)
+//   warp E+1        MMA issuer (one elected thread)
+//   warp E+2        scales: a_scale * b_scale of each block into a small ring
+//
+// Few tiles (decode): the K blocks of a tile are split over the CTAs of a
+// cluster, whose partial sums meet through distributed shared memory in rank
+// order: no workspace, no atomics, the same bits every run.
+// Every mbarrier wait is bounded.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "op_common.cuh"
+#include "tc_common.cuh"
+#include "tma_maps.cuh"
+
+namespace moe {
+namespace {
+
+using namespace op;
+using namespace tc;
+
+constexpr int kWeightRows = 128;            // M of the tile
+constexpr int kABytes = kWeightRows * 128;  // weight rows of a stage (128 columns)
+
+struct ProductArgs {
+    const float *a_scale;
+    int64_t ld_a_scale;
+    const float *b_scale;
+    const int32_t *offsets;  // null: one group of all rows
+    int groups, rows, n, kblocks, n_tiles;
+    void *out;
+    int64_t ld_out;
+    int32_t *status;
+};
+
+template <int BN_, int STAGES_, int BUFS_, int EPI_, int BOX_, int MIN_CTAS_>
+struct Config {
+    static constexpr int BN = BN_;          // widest token tile
+    static constexpr int STAGES = STAGES_;  // operand ring
+    static constexpr int BUFS = BUFS_;      // tensor-memory buffers of BN columns
+    static constexpr int EPI = EPI_;        // epilogue warps (4 or 8)
+    static constexpr int BOX = BOX_;        // token rows of one TMA box
+    static constexpr int MIN_CTAS = MIN_CTAS_;
+    static constexpr int COLS = BN * 4 / EPI;  // columns of an epilogue thread
+    static constexpr int THREADS = 32 * (EPI + 3);
+    static constexpr int SCALES = 4;           // ring of scale rows
+    static constexpr int STAGE_BYTES = kABytes + BN * 128;
+    static constexpr int TABLE = 2 * (kMaxExperts + 1) * 4;  // group offsets, first tiles
+    static constexpr int SMEM = STAGES * STAGE_BYTES + SCALES * BN * 4 + TABLE + 1024;
+    static_assert(STAGES * STAGE_BYTES >= kWeightRows * BN * 4 || MIN_CTAS == 1, "partial tile fits the operand ring");
+};
+typedef Config<64, 4, 4, 4, 16, 2> Narrow;
+typedef Config<256, 4, 2, 8, 64, 1> Wide;
+
+// kind::f8f6f4 instruction descriptor: E4M3 x E4M3 -> f32, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N)
+{
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 16 columns of this thread's tensor-memory lane; the values are valid after tmem_wait16.
+__device__ __forceinline__ void tmem_request16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15])::"memory");
+}
+
+// acc += v * s on a pair
+__device__ __forceinline__ void fma_pair(float2 &acc, uint32_t v0, uint32_t v1, float s0, float s1)
+{
+    asm("{\n\t.reg .b64 rv, rs, ra;\n\t"
+        "mov.b64 rv, {%2, %3};\n\tmov.b64 rs, {%4, %5};\n\tmov.b64 ra, {%0, %1};\n\t"
+        "fma.rn.f32x2 ra, rv, rs, ra;\n\tmov.b64 {%0, %1}, ra;\n\t}"
+        : "+f"(acc.x), "+f"(acc.y)
+        : "r"(v0), "r"(v1), "f"(s0), "f"(s1));
+}
+
+// One output tile: weight rows [n0, n0 + 128) of group g, token rows [row0, row0 + rows).
+struct Tile {
+    int group, n_tile, row0, rows;
+};
+
+__device__ __forceinline__ Tile tile_at(int id, const ProductArgs &a, const int *first_tile, const int *offset, int bn)
+{
+    const int tt = id / a.n_tiles;
+    Tile t;
+    t.n_tile = id - tt * a.n_tiles;
+    int lo = 0, hi = a.groups;  // first_tile[lo] <= tt < first_tile[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first_tile[mid] <= tt) lo = mid;
+        else hi = mid;
+    }
+    t.group = lo;
+    const int i = tt - first_tile[lo], parts = first_tile[lo + 1] - first_tile[lo];
+    const int r = offset[lo + 1] - offset[lo];
+    const int size = (((r + parts - 1) / parts) + 15) & ~15;  // <= bn
+    t.row0 = offset[lo] + i * size;
+    t.rows = min(size, offset[lo] + r - t.row0);  // may be <= 0 for the last part
+    return t;
+}
+
+template <class C, class OUT>
+__global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
+    fp8_product_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                       const ProductArgs a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t full[C::STAGES], empty[C::STAGES], acc_full[C::BUFS], acc_empty[C::BUFS],
+        sc_full[C::SCALES], sc_empty[C::SCALES], drain_bar;
+    __shared__ uint32_t tmem_base;
+    __shared__ int warp_tiles[C::THREADS / 32];
+    __shared__ volatile int abort_flag;
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float *scale_ring = reinterpret_cast<float *>(smem + C::STAGES * C::STAGE_BYTES);
+    int *offset = reinterpret_cast<int *>(scale_ring + C::SCALES * C::BN);
+    int *first_tile = offset + kMaxExperts + 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned rank = cluster_rank(), ranks = cluster_size();
+
+    if (warp == C::EPI + 1) {
+        tmem_alloc(&tmem_base, C::BUFS * C::BN);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < C::BUFS; ++s) {
+            mbar_init(&acc_full[s], 1);
+            mbar_init(&acc_empty[s], C::EPI);
+        }
+        for (int s = 0; s < C::SCALES; ++s) {
+            mbar_init(&sc_full[s], 1);
+            mbar_init(&sc_empty[s], C::EPI);
+        }
+        mbar_init(&drain_bar, 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    // groups: offsets clamped to an ascending sequence inside [0, rows], and each group's first token tile
+    if (!a.offsets) {
+        if (threadIdx.x == 0) {
+            offset[0] = 0;
+            offset[1] = a.rows;
+            first_tile[0] = 0;
+            first_tile[1] = (a.rows + C::BN - 1) / C::BN;
+        }
+    } else {
+        const int per = (a.groups + C::THREADS - 1) / C::THREADS;
+        const int g0 = min(a.groups, (int)threadIdx.x * per), g1 = min(a.groups, g0 + per);
+        int sum = 0;
+        for (int g = g0; g < g1; ++g) {
+            const int lo = min(max(__ldg(a.offsets + g), 0), a.rows);
+            const int hi = min(max(__ldg(a.offsets + g + 1), lo), a.rows);
+            offset[g] = lo;
+            if (g == a.groups - 1) offset[a.groups] = hi;
+            sum += (hi - lo + C::BN - 1) / C::BN;
+        }
+        int scan = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, scan, d);
+            if (lane >= d) scan += v;
+        }
+        if (lane == 31) warp_tiles[warp] = scan;
+        __syncthreads();
+        int run = scan - sum;
+        for (int w = 0; w < warp; ++w) run += warp_tiles[w];
+        for (int g = g0; g < g1; ++g) {
+            first_tile[g] = run;
+            const int lo = offset[g];
+            const int hi = min(max(__ldg(a.offsets + g + 1), lo), a.rows);
+            run += (hi - lo + C::BN - 1) / C::BN;
+            if (g == a.groups - 1) first_tile[a.groups] = run;
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = tmem_base;
+    const int n_work = first_tile[a.groups] * a.n_tiles;
+    const int worker = blockIdx.x / ranks, workers = gridDim.x / ranks;
+    const int kb0 = (int)((int64_t)a.kblocks * rank / ranks), kb1 = (int)((int64_t)a.kblocks * (rank + 1) / ranks);
+    int issued = 0;
+
+    // One tile of each role; a timed-out wait sets abort_flag, after which the
+    // roles skip their work but still meet at the cluster's barriers.
+    int it = 0, sit = 0;  // this role's position in the operand ring / the block sequence
+    for (int id = worker; id < n_work; id += workers) {
+        const Tile t = tile_at(id, a, first_tile, offset, C::BN);
+        const int ncols = (max(t.rows, 1) + 15) & ~15;
+        float2 acc[C::COLS / 2];
+        if (warp == C::EPI) {  // ---- TMA producer
+            if (lane == 0) {
+                const int boxes = (ncols + C::BOX - 1) / C::BOX;
+                for (int kb = kb0; kb < kb1 && !abort_flag; ++kb, ++it) {
+                    const int s = it % C::STAGES, u = it / C::STAGES;
+                    if (u > 0 && !mbar_wait(&empty[s], (u - 1) & 1)) {
+                        abort_flag = 1;
+                        break;
+                    }
+                    uint8_t *w_s = smem + s * C::STAGE_BYTES, *x_s = w_s + kABytes;
+                    mbar_arrive_expect_tx(&full[s], kABytes + boxes * C::BOX * 128);
+                    tma_load_3d(w_s, &map_w, &full[s], kb * 128, t.n_tile * kWeightRows, t.group);
+                    for (int b = 0; b < boxes; ++b)
+                        tma_load_2d(x_s + b * C::BOX * 128, &map_x, &full[s], kb * 128, t.row0 + b * C::BOX);
+                }
+                issued = it;
+            }
+        } else if (warp == C::EPI + 1) {  // ---- MMA issuer
+            if (lane == 0) {
+                const uint32_t idesc = idesc_e4m3(kWeightRows, ncols);
+                for (int kb = kb0; kb < kb1 && !abort_flag; ++kb, ++it) {
+                    const int s = it % C::STAGES, u = it / C::STAGES;
+                    const int d = it % C::BUFS, du = it / C::BUFS;
+                    if ((du > 0 && !mbar_wait(&acc_empty[d], (du - 1) & 1)) || !mbar_wait(&full[s], u & 1)) {
+                        abort_flag = 1;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint64_t wd = desc_kmajor_sw128(smem + s * C::STAGE_BYTES);
+                    const uint64_t xd = desc_kmajor_sw128(smem + s * C::STAGE_BYTES + kABytes);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) mma_f8(tmem + d * C::BN, wd + 2 * kk, xd + 2 * kk, idesc, kk != 0);
+                    mma_commit(&empty[s]);
+                    mma_commit(&acc_full[d]);
+                }
+            }
+        } else if (warp == C::EPI + 2) {  // ---- scales
+            constexpr int PER = (C::BN + 31) / 32;  // columns of a lane
+            constexpr int AHEAD = 16 / PER > 4 ? 4 : 16 / PER;
+            const float *bs = a.b_scale + ((int64_t)t.group * a.n_tiles + t.n_tile) * a.kblocks;
+            bool go = true;
+            for (int k0 = kb0; k0 < kb1 && go; k0 += AHEAD) {
+                float v[AHEAD][PER];
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    const float w = k0 + i < kb1 ? __ldg(bs + k0 + i) : 0.f;
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) {
+                        const int c = j * 32 + lane;
+                        v[i][j] = k0 + i < kb1 && c < t.rows
+                                      ? w * __ldg(a.a_scale + (int64_t)(k0 + i) * a.ld_a_scale + t.row0 + c)
+                                      : 0.f;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    if (k0 + i >= kb1) break;
+                    const int s = sit % C::SCALES, u = sit / C::SCALES;
+                    ++sit;
+                    if (lane == 0) {
+                        go = !abort_flag && (u == 0 || mbar_wait(&sc_empty[s], (u - 1) & 1));
+                        if (!go) abort_flag = 1;
+                    }
+                    go = __shfl_sync(0xffffffffu, go, 0);
+                    if (!go) break;
+#pragma unroll
+                    for (int j = 0; j < PER; ++j)
+                        if (j * 32 + lane < C::BN) scale_ring[s * C::BN + j * 32 + lane] = v[i][j];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sc_full[s]);
+                }
+            }
+        } else {  // ---- epilogue warps
+            const int part = warp >> 2, c0 = part * C::COLS;
+#pragma unroll
+            for (int i = 0; i < C::COLS / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const int d = it % C::BUFS, s = it % C::SCALES;
+                const bool ok = !abort_flag && mbar_wait(&acc_full[d], (it / C::BUFS) & 1) &&
+                                mbar_wait(&sc_full[s], (it / C::SCALES) & 1);
+                tc_fence_after_sync();
+                if (!__all_sync(0xffffffffu, ok)) {
+                    abort_flag = 1;
+                    break;
+                }
+                const uint32_t td = tmem + d * C::BN + c0 + ((uint32_t)((warp & 3) * 32) << 16);
+                const float *sc = scale_ring + s * C::BN + c0;
+#pragma unroll
+                for (int c = 0; c < C::COLS; c += 16) {
+                    if (c0 + c < ncols) {
+                        uint32_t v[16];
+                        tmem_request16(td + c, v);
+                        tmem_wait16(v);
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(sc + c + j);
+                            fma_pair(acc[(c + j) / 2], v[j], v[j + 1], f.x, f.y);
+                            fma_pair(acc[(c + j) / 2 + 1], v[j + 2], v[j + 3], f.z, f.w);
+                        }
+                    }
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&acc_empty[d]);
+                    mbar_arrive(&sc_empty[s]);
+                }
+            }
+        }
+        __syncwarp();
+        if (ranks > 1) {
+            // partial sums of the cluster's CTAs, added in rank order; the operand ring is
+            // idle here (its last block has been multiplied) and holds this CTA's partial
+            float *partial = reinterpret_cast<float *>(smem);  // [column][weight row]
+            if (warp < C::EPI) {
+                const int c0 = (warp >> 2) * C::COLS, m = (warp & 3) * 32 + lane;
+#pragma unroll
+                for (int i = 0; i < C::COLS / 2; ++i) {
+                    if (c0 + 2 * i < ncols) {
+                        partial[(c0 + 2 * i) * kWeightRows + m] = acc[i].x;
+                        partial[(c0 + 2 * i + 1) * kWeightRows + m] = acc[i].y;
+                    }
+                }
+            }
+            cluster_sync();
+            if (warp < C::EPI && !abort_flag) {
+                const int n = t.n_tile * kWeightRows + (threadIdx.x & 127);
+                for (int c = (int)rank * (C::EPI / 4) + (threadIdx.x >> 7); c < t.rows; c += ranks * (C::EPI / 4)) {
+                    const uint32_t at = smem_u32(partial + c * kWeightRows + (threadIdx.x & 127));
+                    float v = 0.f;
+                    for (unsigned r = 0; r < ranks; ++r) v += cluster_ld_f32(cluster_map(at, r));
+                    if (n < a.n) static_cast<OUT *>(a.out)[(int64_t)(t.row0 + c) * a.ld_out + n] = OUT(v);
+                }
+            }
+            fence_proxy_async_smem();  // the ring is written by TMA again
+            cluster_sync();
+        } else if (warp < C::EPI && !abort_flag) {
+            const int c0 = (warp >> 2) * C::COLS, n = t.n_tile * kWeightRows + (warp & 3) * 32 + lane;
+            if (n < a.n) {
+                OUT *out = static_cast<OUT *>(a.out) + (int64_t)(t.row0 + c0) * a.ld_out + n;
+#pragma unroll
+                for (int i = 0; i < C::COLS / 2; ++i) {
+                    if (c0 + 2 * i < t.rows) out[(int64_t)(2 * i) * a.ld_out] = OUT(acc[i].x);
+                    if (c0 + 2 * i + 1 < t.rows) out[(int64_t)(2 * i + 1) * a.ld_out] = OUT(acc[i].y);
+                }
+            }
+        }
+    }
+    // after a timed-out wait: let copies and MMAs in flight land before memory is released
+    if (abort_flag) {
+        if (warp == C::EPI && lane == 0) drain_ring(full, C::STAGES, issued);
+        if (warp == C::EPI + 1 && lane == 0) drain_mma(&drain_bar);
+        if (threadIdx.x == 0 && a.status) atomicExch(a.status, (int)MOE_ERR_TIMEOUT);
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == C::EPI + 1) tmem_dealloc(tmem, C::BUFS * C::BN);
+}
+
+// uint8 rows of `cols` codes, row stride ld bytes; boxes of 128 columns in the 128-byte swizzle
+bool code_map(CUtensorMap *m, const void *base, int cols, int64_t rows, int64_t ld, int64_t groups, int64_t stride,
+              int box_rows)
+{
+    const tmaps::EncodeTiledFn f = tmaps::encode_fn();
+    if (!f) return false;
+    const int dim = groups > 0 ? 3 : 2;
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)groups};
+    cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)stride};
+    cuuint32_t box[3] = {128, (cuuint32_t)box_rows, 1}, es[3] = {1, 1, 1};
+    return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, dim, const_cast<void *>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Operands {
+    const uint8_t *a, *b;
+    int64_t ld_a, ld_b, stride_b;
+    int k;
+};
+
+template <class C>
+cudaError_t set_smem()
+{
+    cudaError_t e = cudaFuncSetAttribute(fp8_product_kernel<C, float>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(fp8_product_kernel<C, __nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+}
+
+template <class C>
+moe_status run_product(const Operands &o, const ProductArgs &a, moe_dtype out_dtype, int workers, int ranks,
+                       cudaStream_t s)
+{
+    CUtensorMap mw, mx;
+    if (!code_map(&mw, o.b, o.k, a.n, o.ld_b, a.groups, o.stride_b, kWeightRows)) return MOE_ERR_CUDA;
+    if (!code_map(&mx, o.a, o.k, a.rows, o.ld_a, 0, 0, C::BOX)) return MOE_ERR_CUDA;
+    const dim3 grid(workers * ranks);
+    return launched(out_dtype == MOE_DT_BF16 ? launch(fp8_product_kernel<C, __nv_bfloat16>, grid, C::THREADS, C::SMEM, s,
+                                                      ranks, false, mw, mx, a)
+                                             : launch(fp8_product_kernel<C, float>, grid, C::THREADS, C::SMEM, s, ranks,
+                                                      false, mw, mx, a));
+}
+
+PerDevice g_product;
+
+cudaError_t product_prepare()
+{
+    if (!tmaps::encode_fn()) return cudaErrorUnknown;
+    const cudaError_t e = set_smem<Narrow>();
+    return e != cudaSuccess ? e : set_smem<Wide>();
+}
+
+moe_status product(const uint8_t *a, int64_t ld_a, const float *a_scale, int64_t ld_a_scale, int rows, const uint8_t *b,
+                   int64_t ld_b, int64_t stride_b, const float *b_scale, const int32_t *offsets, int groups, int n,
+                   int k, void *out, moe_dtype out_dtype, int64_t ld_out, int32_t *status, void *stream)
+{
+    if (out_dtype != MOE_DT_F32 && out_dtype != MOE_DT_BF16) return MOE_ERR_INVALID_ARG;
+    if (rows < 0 || n < 1 || n > (1 << 20) || k < 1 || k > (1 << 20) || groups < 1 || groups > kMaxExperts)
+        return MOE_ERR_INVALID_ARG;
+    if (ld_a < k || ld_a % 16 || ld_b < k || ld_b % 16 || stride_b % 16 || ld_out < n || ld_a_scale < rows)
+        return MOE_ERR_INVALID_ARG;
+    if (ld_a >= 1ll << 40 || ld_b >= 1ll << 40 || stride_b >= 1ll << 40) return MOE_ERR_INVALID_ARG;
+    if (groups > 1 && stride_b < n * ld_b) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!a || !a_scale || !b || !b_scale || !out) return MOE_ERR_INVALID_ARG;
+    if (!aligned(a, 16) || !aligned(b, 16) || !aligned(a_scale, 4) || !aligned(b_scale, 4) || !aligned(offsets, 4) ||
+        !aligned(out, out_dtype == MOE_DT_BF16 ? 2 : 4) || !aligned(status, 4))
+        return MOE_ERR_INVALID_ARG;
+    ProductArgs p{};
+    p.a_scale = a_scale;
+    p.ld_a_scale = ld_a_scale;
+    p.b_scale = b_scale;
+    p.offsets = offsets;
+    p.groups = groups;
+    p.rows = rows;
+    p.n = n;
+    p.kblocks = ceil_div(k, kScaleBlock);
+    p.n_tiles = ceil_div(n, kWeightRows);
+    p.out = out;
+    p.ld_out = ld_out;
+    p.status = status;
+    int sms = 0;
+    const moe_status st = g_product.get(&sms, product_prepare);
+    if (st != MOE_OK) return st;
+    const Operands o{a, b, ld_a, ld_b, stride_b ? stride_b : ld_b, k};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // most tiles that any offsets could give: one per non-empty group and one per further full tile
+    const auto most_tiles = [&](int bn) {
+        const int64_t used = std::min<int64_t>(groups, rows);
+        return std::min<int64_t>(rows, used + (rows - used) / bn) * p.n_tiles;
+    };
+    if (most_tiles(Narrow::BN) > INT32_MAX) return MOE_ERR_INVALID_ARG;
+    const int64_t wide = most_tiles(Wide::BN);
+    const bool few_rows = (int64_t)rows <= 32ll * groups || wide < sms;
+    if (!few_rows) return run_product<Wide>(o, p, out_dtype, (int)std::min<int64_t>(wide, sms), 1, s);
+    const int64_t narrow = most_tiles(Narrow::BN);
+    const int slots = 2 * sms;
+    int ranks = 1;
+    while (ranks < 8 && narrow * ranks * 2 <= slots && ranks * 2 <= p.kblocks) ranks *= 2;
+    return run_product<Narrow>(o, p, out_dtype, (int)std::min<int64_t>(narrow, slots / ranks), ranks, s);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_fp8_matmul(const uint8_t *a, int64_t ld_a, const float *a_scale, int64_t ld_a_scale, int rows,
+                                     const uint8_t *b, int64_t ld_b, const float *b_scale, int n, int k, void *out,
+                                     moe_dtype out_dtype, int64_t ld_out, int32_t *status, void *stream)
+{
+    return product(a, ld_a, a_scale, ld_a_scale, rows, b, ld_b, 0, b_scale, nullptr, 1, n, k, out, out_dtype, ld_out,
+                   status, stream);
+}
+
+extern "C" moe_status moe_fp8_grouped_matmul(const uint8_t *a, int64_t ld_a, const float *a_scale, int64_t ld_a_scale,
+                                             int rows, const uint8_t *b, int64_t ld_b, int64_t group_stride_b,
+                                             const float *b_scale, const int32_t *offsets, int n_groups, int n, int k,
+                                             void *out, moe_dtype out_dtype, int64_t ld_out, int32_t *status,
+                                             void *stream)
+{
+    if (!offsets) return MOE_ERR_INVALID_ARG;
+    return product(a, ld_a, a_scale, ld_a_scale, rows, b, ld_b, group_stride_b, b_scale, offsets, n_groups, n, k, out,
+                   out_dtype, ld_out, status, stream);
+}

@@ -1,0 +1,277 @@
+// Quantisers to E4M3 codes with an fp32 scale per block of 128.
+//
+//   a     = max(max |x| over the block, 448 * 2^-126)
+//   scale = a / 448,   code = E4M3(x * (448 / a))     (nearest even)
+//
+// in fp32, so scale * code is x within half an E4M3 step of the block's largest
+// magnitude's scale, and 448 / a and the product never overflow.  The floor
+// keeps an all-zero block at codes 0 (its scale is 2^-126).  A NaN or infinity
+// makes its whole block NaN.  Blocks are 128 columns of one row (activations)
+// or 128 rows x 128 columns (weights); the last ones may be shorter.
+//
+// Activations may be gathered (output row r is source row rows[r]) or be the
+// SwiGLU of a gate/up row, silu(x[:cols]) * x[cols:], so that neither the
+// gathered rows nor h is ever written: bytes are one read of the source and one
+// write of codes and scales.  Half a warp owns a block: eight values a lane,
+// four shuffles for the maximum.  A CTA takes 8 rows by all their blocks, so
+// the scales of a block (stored block by block over the rows, the layout the
+// product reads) leave as whole 32-byte sectors.
+#include <algorithm>
+
+#include "op_common.cuh"
+
+namespace moe {
+namespace {
+
+using namespace op;
+
+constexpr float kE4m3Max = 448.f;
+constexpr float kAmaxFloor = 448.f * 1.17549435e-38f;  // 448 * 2^-126
+constexpr int kQuantThreads = 256, kQuantRows = 8;
+
+__device__ __forceinline__ void block_scale(uint32_t amax_bits, float &scale, float &inv)
+{
+    // amax as bits of |x|: integer order puts NaN above infinity, so it survives
+    float a = __uint_as_float(amax_bits);
+    a = a < kAmaxFloor ? kAmaxFloor : a;
+    scale = __fdiv_rn(a, kE4m3Max);
+    inv = __fdiv_rn(kE4m3Max, a);
+}
+
+// two E4M3 codes (lo in the low byte), round to nearest even, |x| <= 448
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + expf(-g)); }
+
+template <class T>
+__device__ __forceinline__ void load8(const T *p, float (&v)[8]);
+template <>
+__device__ __forceinline__ void load8<float>(const float *p, float (&v)[8])
+{
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+template <>
+__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, float (&v)[8])
+{
+    const uint4 r = __ldg(reinterpret_cast<const uint4 *>(p));
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ float as_float(float v) { return v; }
+__device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+struct QuantArgs {
+    const void *x;
+    int64_t ld_x;
+    const int32_t *index;  // output row -> source row, or null
+    int src_rows, rows, cols, blocks;
+    uint8_t *codes;
+    int64_t ld_codes;
+    float *scales;
+    int64_t ld_scales;
+};
+
+// eight consecutive values of a row from column c0 (zero from `cols` on)
+template <class T, bool WIDE>
+__device__ __forceinline__ void load_values(const T *row, int c0, int cols, float (&v)[8])
+{
+    if (WIDE && c0 + 8 <= cols) {
+        load8<T>(row + c0, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = c0 + j < cols ? as_float(row[c0 + j]) : 0.f;
+    }
+}
+
+template <class T, bool SWIGLU, bool WIDE>
+__global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const QuantArgs a)
+{
+    const int half = threadIdx.x >> 4, lane = threadIdx.x & 15;
+    const int row = blockIdx.x * kQuantRows + (half & (kQuantRows - 1));
+    const T *x = nullptr;
+    if (row < a.rows) {
+        const int src = a.index ? __ldg(a.index + row) : row;
+        if ((unsigned)src < (unsigned)a.src_rows) x = static_cast<const T *>(a.x) + (int64_t)src * a.ld_x;
+    }
+    const int per = kQuantThreads / 16 / kQuantRows;  // blocks of a row in flight
+    for (int b = half / kQuantRows + blockIdx.y * per; b < a.blocks; b += per * gridDim.y) {
+        const int c0 = b * kScaleBlock + lane * 8;
+        float v[8];
+        if (x) {
+            load_values<T, WIDE>(x, c0, a.cols, v);
+            if (SWIGLU) {
+                float u[8];
+                load_values<T, WIDE>(x + a.cols, c0, a.cols, u);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = silu(v[j]) * u[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = 0.f;
+        }
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
+#pragma unroll
+        for (int d = 8; d; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+        float scale, inv;
+        block_scale(m, scale, inv);
+        if (row >= a.rows) continue;
+        uint2 q;
+        q.x = e4m3x2(v[0] * inv, v[1] * inv) | e4m3x2(v[2] * inv, v[3] * inv) << 16;
+        q.y = e4m3x2(v[4] * inv, v[5] * inv) | e4m3x2(v[6] * inv, v[7] * inv) << 16;
+        uint8_t *dst = a.codes + (int64_t)row * a.ld_codes + c0;
+        if (c0 + 8 <= a.cols) {
+            *reinterpret_cast<uint2 *>(dst) = q;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c0 + j < a.cols) dst[j] = (uint8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+        }
+        if (lane == 0) a.scales[(int64_t)b * a.ld_scales + row] = scale;
+    }
+}
+
+// One CTA per 128 x 128 block: thread t holds 8 columns of rows t / 16 + 16 i.
+template <class T, bool WIDE>
+__global__ void __launch_bounds__(kQuantThreads)
+    quantize_weight_kernel(const T *__restrict__ w, int64_t ld_w, int64_t group_stride, int n, int cols,
+                           uint8_t *__restrict__ codes, int64_t ld_codes, int64_t codes_stride,
+                           float *__restrict__ scales)
+{
+    __shared__ uint32_t red[kQuantThreads / 32];
+    const int kb = blockIdx.x, nb = blockIdx.y, g = blockIdx.z;
+    const int c0 = kb * kScaleBlock + (threadIdx.x & 15) * 8;
+    const int r0 = nb * kScaleBlock + (threadIdx.x >> 4);
+    const T *src = w + (int64_t)g * group_stride;
+    float v[8][8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = r0 + 16 * i;
+        if (r < n) {
+            load_values<T, WIDE>(src + (int64_t)r * ld_w, c0, cols, v[i]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[i][j]));
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kQuantThreads / 32; ++i) m = max(m, red[i]);
+    float scale, inv;
+    block_scale(m, scale, inv);
+    if (threadIdx.x == 0) scales[((int64_t)g * gridDim.y + nb) * gridDim.x + kb] = scale;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = r0 + 16 * i;
+        if (r >= n) continue;
+        uint2 q;
+        q.x = e4m3x2(v[i][0] * inv, v[i][1] * inv) | e4m3x2(v[i][2] * inv, v[i][3] * inv) << 16;
+        q.y = e4m3x2(v[i][4] * inv, v[i][5] * inv) | e4m3x2(v[i][6] * inv, v[i][7] * inv) << 16;
+        uint8_t *dst = codes + (int64_t)g * codes_stride + (int64_t)r * ld_codes + c0;
+        if (c0 + 8 <= cols) {
+            *reinterpret_cast<uint2 *>(dst) = q;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c0 + j < cols) dst[j] = (uint8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+        }
+    }
+}
+
+typedef void (*QuantKernel)(const QuantArgs);
+
+template <class T>
+QuantKernel quant_pick(bool swiglu, bool wide)
+{
+    if (swiglu) return wide ? quantize_rows_kernel<T, true, true> : quantize_rows_kernel<T, true, false>;
+    return wide ? quantize_rows_kernel<T, false, true> : quantize_rows_kernel<T, false, false>;
+}
+
+unsigned dtype_size(moe_dtype dt) { return dt == MOE_DT_BF16 ? 2 : 4; }
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_fp8_quantize(const void *x, moe_dtype x_dtype, int64_t ld_x, const int32_t *rows,
+                                       int n_src_rows, int n_rows, int cols, int swiglu, uint8_t *codes,
+                                       int64_t ld_codes, float *scales, int64_t ld_scales, void *stream)
+{
+    if ((x_dtype != MOE_DT_F32 && x_dtype != MOE_DT_BF16) || (swiglu != 0 && swiglu != 1)) return MOE_ERR_INVALID_ARG;
+    if (n_rows < 0 || n_src_rows < 0 || cols < 1 || cols > (1 << 20)) return MOE_ERR_INVALID_ARG;
+    if (!rows && n_src_rows != n_rows) return MOE_ERR_INVALID_ARG;
+    if (ld_x < (swiglu ? 2 : 1) * (int64_t)cols || ld_codes < cols || ld_codes % 16 || ld_scales < n_rows)
+        return MOE_ERR_INVALID_ARG;
+    if (n_rows == 0) return MOE_OK;
+    if (!codes || !scales || (!x && n_src_rows)) return MOE_ERR_INVALID_ARG;
+    const unsigned size = dtype_size(x_dtype);
+    if (!aligned(x, size) || !aligned(rows, 4) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_ERR_INVALID_ARG;
+    QuantArgs a{};
+    a.x = x;
+    a.ld_x = ld_x;
+    a.index = rows;
+    a.src_rows = n_src_rows;
+    a.rows = n_rows;
+    a.cols = cols;
+    a.blocks = ceil_div(cols, kScaleBlock);
+    a.codes = codes;
+    a.ld_codes = ld_codes;
+    a.scales = scales;
+    a.ld_scales = ld_scales;
+    // 16-byte loads where every block of every row (and of its up half) starts on one
+    const bool wide = aligned(x, 16) && ld_x * size % 16 == 0 && (!swiglu || (int64_t)cols * size % 16 == 0);
+    QuantKernel f = x_dtype == MOE_DT_BF16 ? quant_pick<__nv_bfloat16>(swiglu, wide) : quant_pick<float>(swiglu, wide);
+    const int row_ctas = ceil_div(n_rows, kQuantRows);
+    // few rows: one CTA per pair of blocks; many: a CTA walks its rows' blocks
+    const int by = std::max(1, std::min(ceil_div(a.blocks, kQuantThreads / 16 / kQuantRows), 1184 / row_ctas));
+    f<<<dim3(row_ctas, by), kQuantThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    return launched(cudaGetLastError());
+}
+
+extern "C" moe_status moe_fp8_quantize_weight(const void *w, moe_dtype w_dtype, int64_t ld_w, int64_t group_stride_w,
+                                              int n_groups, int n, int cols, uint8_t *codes, int64_t ld_codes,
+                                              int64_t group_stride_codes, float *scales, void *stream)
+{
+    if (w_dtype != MOE_DT_F32 && w_dtype != MOE_DT_BF16) return MOE_ERR_INVALID_ARG;
+    if (n_groups < 0 || n_groups > 65535 || n < 0 || n > (1 << 20) || cols < 1 || cols > (1 << 20))
+        return MOE_ERR_INVALID_ARG;
+    if (ld_w < cols || ld_codes < cols || ld_codes % 16 || group_stride_codes % 16) return MOE_ERR_INVALID_ARG;
+    if (n_groups > 1 && (group_stride_w < n * ld_w || group_stride_codes < n * ld_codes)) return MOE_ERR_INVALID_ARG;
+    if (n_groups == 0 || n == 0) return MOE_OK;
+    if (!w || !codes || !scales) return MOE_ERR_INVALID_ARG;
+    const unsigned size = dtype_size(w_dtype);
+    if (!aligned(w, size) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_ERR_INVALID_ARG;
+    const bool wide = aligned(w, 16) && ld_w * size % 16 == 0 && group_stride_w * size % 16 == 0;
+    const dim3 grid(ceil_div(cols, kScaleBlock), ceil_div(n, kScaleBlock), n_groups);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (w_dtype == MOE_DT_BF16) {
+        auto f = wide ? quantize_weight_kernel<__nv_bfloat16, true> : quantize_weight_kernel<__nv_bfloat16, false>;
+        f<<<grid, kQuantThreads, 0, s>>>(static_cast<const __nv_bfloat16 *>(w), ld_w, group_stride_w, n, cols, codes,
+                                         ld_codes, group_stride_codes, scales);
+    } else {
+        auto f = wide ? quantize_weight_kernel<float, true> : quantize_weight_kernel<float, false>;
+        f<<<grid, kQuantThreads, 0, s>>>(static_cast<const float *>(w), ld_w, group_stride_w, n, cols, codes, ld_codes,
+                                         group_stride_codes, scales);
+    }
+    return launched(cudaGetLastError());
+}

@@ -386,6 +386,140 @@ moe_status moe_debug_dequant_rows(const moe_pack *pack, int proj, int slot, int 
 moe_status moe_debug_tail_plan(int n_tokens, int max_tokens, int hidden, int n_experts, int inter, int top_k,
                                moe_dtype x_dtype, moe_fmt fmt_gate_up, moe_fmt fmt_down, int grid, int64_t *out);
 
+/* ---- operators beside the layer: the expert plan, the router's balance loss,
+ * and products in 8-bit floating point -------------------------------------------
+ *
+ * What a user composes around the layer's own path: moe_route_topk gives each
+ * token its experts; moe_expert_plan sorts the (token, choice) pairs by expert;
+ * moe_fp8_quantize gathers the tokens into that order as E4M3 codes;
+ * moe_fp8_grouped_matmul multiplies each expert's rows by its weights;
+ * moe_fp8_quantize (swiglu) turns gate/up rows into the next product's
+ * operand; moe_balance_loss and its gradient keep the routing even in
+ * training.
+ *
+ * All of them only enqueue on `stream`: no allocation, no host
+ * synchronisation, capturable.  Pointers are device memory of the calling
+ * thread's current device and are aligned to their element unless an entry
+ * says otherwise.  Nothing is kept from one call for the next.  Outputs do not
+ * overlap inputs. */
+
+/* Pairs sorted by expert.  Pair p = t * top_k + j is choice j of token t.
+ *   idx      device [n_tokens x top_k] int32 (as moe_route_topk writes it); a
+ *            value outside [0, n_experts) is no choice (padding): it has no
+ *            slot.  One token may name an expert more than once.
+ *   counts   device [n_experts]: pairs of each expert
+ *   offsets  device [n_experts + 1]: first slot of each expert; the last entry
+ *            is the number of slots in use
+ *   rows     device [n_tokens * top_k]: token of each slot, -1 from the last
+ *            slot in use on
+ *   slots    device [n_tokens x top_k]: slot of each pair, -1 for no choice
+ * Slots of one expert follow the pairs' order.  1 <= top_k <= n_experts <=
+ * 1024, n_tokens * top_k <= 2^30.  n_tokens == 0 writes zero counts and
+ * offsets; idx, rows and slots are then not touched and may be NULL. */
+moe_status moe_expert_plan(const int32_t *idx, int n_tokens, int top_k, int n_experts, int32_t *counts,
+                           int32_t *offsets, int32_t *rows, int32_t *slots, void *stream);
+
+/* Workspace bytes moe_balance_loss needs (0 for small batches). */
+size_t moe_balance_loss_workspace_bytes(int n_tokens, int n_experts);
+
+/* Balance loss of a router.  With n tokens that count, p = softmax(logits) per
+ * token and c_e their choices of expert e:
+ *   P_e = 1/n sum_t p_te,  f_e = n_experts * c_e / (top_k * n),  loss = sum_e f_e P_e
+ * (1 when choices and probabilities are even, n_experts when all fall on one).
+ *   logits    device [n_tokens x n_experts] fp32 or bf16, row-major
+ *   idx       device [n_tokens x top_k] int32; values outside [0, n_experts)
+ *             are no choice
+ *   valid     device [n_tokens] bytes: 0 = the token does not count (padding;
+ *             its logits and choices are not used), or NULL: all count
+ *   loss      device [1] fp32
+ *   counts    device [n_experts + 1] int32: c_e, then n
+ *   prob_mean device [n_experts] fp32: P_e
+ *   workspace device, 16-byte aligned, moe_balance_loss_workspace_bytes bytes
+ *             (NULL when that is 0); its contents need no initialisation.  Two
+ *             calls that may run at the same time need one each.
+ * A logit of -inf has probability 0; a token whose logits are all -inf adds
+ * nothing to P.  With no token that counts, loss, counts and P are 0.  Sums
+ * are fp32 in a fixed order: results are reproducible bit for bit. */
+moe_status moe_balance_loss(const void *logits, moe_dtype dtype, const int32_t *idx, const uint8_t *valid,
+                            int n_tokens, int n_experts, int top_k, float *loss, int32_t *counts, float *prob_mean,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* Its gradient (the choices have none):
+ *   dlogits_te = dloss * p_te * (f_e - sum_j f_j p_tj) / n
+ *   counts   as moe_balance_loss wrote them
+ *   dloss    device [1] fp32: gradient of the loss (its weight in training)
+ *   dlogits  device [n_tokens x n_experts], type of logits; rows of tokens
+ *            that do not count become 0 */
+moe_status moe_balance_loss_backward(const void *logits, moe_dtype dtype, const int32_t *counts, const uint8_t *valid,
+                                     const float *dloss, int n_tokens, int n_experts, int top_k, void *dlogits,
+                                     void *stream);
+
+/* E4M3 codes (1 sign, 4 exponent, 3 mantissa bits, no infinities) with an fp32
+ * scale per block of 128 columns; value = scale * code.  Per block
+ *   a = max(max |x|, 448 * 2^-126),  scale = a / 448,  code = E4M3(x * (448 / a))
+ * in fp32, codes rounded to nearest even.  An all-zero block has codes 0; a NaN
+ * or infinity makes its block NaN.
+ *   x       device, n_src_rows rows of cols values (swiglu: 2 * cols), fp32 or
+ *           bf16, row stride ld_x elements
+ *   rows    device [n_rows] int32: source row of each output row (a value
+ *           outside [0, n_src_rows) gives a row of zeros), or NULL: output row
+ *           r is source row r (n_src_rows == n_rows)
+ *   swiglu  0, or 1: the value is silu(x[c]) * x[cols + c], in fp32
+ *   codes   device [n_rows x cols] bytes, row stride ld_codes (a multiple of
+ *           16), 16-byte aligned; bytes between cols and ld_codes are not
+ *           written
+ *   scales  device [ceil(cols / 128) x n_rows] fp32, one row per block, row
+ *           stride ld_scales elements
+ * 1 <= cols <= 2^20.  n_rows == 0 enqueues nothing. */
+moe_status moe_fp8_quantize(const void *x, moe_dtype x_dtype, int64_t ld_x, const int32_t *rows, int n_src_rows,
+                            int n_rows, int cols, int swiglu, uint8_t *codes, int64_t ld_codes, float *scales,
+                            int64_t ld_scales, void *stream);
+
+/* The same for weights, with a scale per 128 rows x 128 columns.
+ *   w       device, n_groups matrices of [n x cols], fp32 or bf16, row stride
+ *           ld_w and matrix stride group_stride_w in elements
+ *   codes   device, n_groups x [n x cols] bytes, strides in bytes, multiples
+ *           of 16, 16-byte aligned
+ *   scales  device [n_groups x ceil(n / 128) x ceil(cols / 128)] fp32
+ * n and cols <= 2^20, n_groups <= 65535. */
+moe_status moe_fp8_quantize_weight(const void *w, moe_dtype w_dtype, int64_t ld_w, int64_t group_stride_w, int n_groups,
+                                   int n, int cols, uint8_t *codes, int64_t ld_codes, int64_t group_stride_codes,
+                                   float *scales, void *stream);
+
+/* out[r, j] = sum over blocks i of 128 columns of
+ *   a_scale[i, r] * b_scale[j / 128, i] * sum_{c in block i} a[r, c] * b[j, c]
+ * with fp32 sums, rounded once to the output's type.
+ *   a        device [rows x k] E4M3 codes, row stride ld_a bytes
+ *   a_scale  device [ceil(k / 128) x rows] fp32, row stride ld_a_scale
+ *            elements (as moe_fp8_quantize writes them)
+ *   b        device [n x k] E4M3 codes, row stride ld_b bytes
+ *   b_scale  device [ceil(n / 128) x ceil(k / 128)] fp32
+ *   out      device [rows x n] fp32 or bf16, row stride ld_out elements
+ *   status   device int32, or NULL: MOE_ERR_TIMEOUT is stored there if a
+ *            bounded wait of the kernel runs out (outputs are then undefined);
+ *            otherwise it is not written
+ * a and b are 16-byte aligned and their row strides multiples of 16; n and k
+ * are any sizes up to 2^20.  rows == 0 enqueues nothing.  The product by the
+ * transposed weights (the gradient of a) is the same call on the transposed
+ * codes and block scales. */
+moe_status moe_fp8_matmul(const uint8_t *a, int64_t ld_a, const float *a_scale, int64_t ld_a_scale, int rows,
+                          const uint8_t *b, int64_t ld_b, const float *b_scale, int n, int k, void *out,
+                          moe_dtype out_dtype, int64_t ld_out, int32_t *status, void *stream);
+
+/* Rows [offsets[g], offsets[g + 1]) times the transpose of matrix g.
+ *   offsets  device [n_groups + 1] int32, ascending, within [0, rows] (as
+ *            moe_expert_plan writes them; other values are clamped into that
+ *            range).  Rows before the first and behind the last offset are not
+ *            read and their outputs are left as they were.
+ *   b        device, n_groups matrices [n x k], group_stride_b bytes apart (a
+ *            multiple of 16)
+ *   b_scale  device [n_groups x ceil(n / 128) x ceil(k / 128)] fp32
+ * 1 <= n_groups <= 1024; the other arguments as moe_fp8_matmul. */
+moe_status moe_fp8_grouped_matmul(const uint8_t *a, int64_t ld_a, const float *a_scale, int64_t ld_a_scale, int rows,
+                                  const uint8_t *b, int64_t ld_b, int64_t group_stride_b, const float *b_scale,
+                                  const int32_t *offsets, int n_groups, int n, int k, void *out, moe_dtype out_dtype,
+                                  int64_t ld_out, int32_t *status, void *stream);
+
 /* Sticky device-side error of the pack (synchronises its device), then clears it. */
 moe_status moe_get_device_error(const moe_pack *pack);
 
