@@ -29,33 +29,12 @@
 // cluster, whose partial sums meet through distributed shared memory in rank
 // order: no workspace, no atomics, the same bits every run.
 // Every mbarrier wait is bounded.
-#include <cuda.h>
-
-#include <algorithm>
-
-#include "op_common.cuh"
-#include "tc_common.cuh"
-#include "tma_maps.cuh"
+#include "fp8_common.cuh"
 
 namespace moe {
 namespace {
 
-using namespace op;
-using namespace tc;
-
-constexpr int kWeightRows = 128;            // M of the tile
-constexpr int kABytes = kWeightRows * 128;  // weight rows of a stage (128 columns)
-
-struct ProductArgs {
-    const float *a_scale;
-    int64_t ld_a_scale;
-    const float *b_scale;
-    const int32_t *offsets;  // null: one group of all rows
-    int groups, rows, n, kblocks, n_tiles;
-    void *out;
-    int64_t ld_out;
-    int32_t *status;
-};
+using namespace fp8;
 
 template <int BN_, int STAGES_, int BUFS_, int EPI_, int BOX_, int MIN_CTAS_>
 struct Config {
@@ -74,13 +53,6 @@ struct Config {
     static_assert(STAGES * STAGE_BYTES >= kWeightRows * BN * 4 || MIN_CTAS == 1, "partial tile fits the operand ring");
 };
 typedef Config<64, 4, 4, 4, 16, 2> Narrow;
-typedef Config<256, 4, 2, 8, 64, 1> Wide;
-
-// kind::f8f6f4 instruction descriptor: E4M3 x E4M3 -> f32, both K-major.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N)
-{
-    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
 
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                        uint32_t accumulate)
@@ -119,31 +91,6 @@ __device__ __forceinline__ void fma_pair(float2 &acc, uint32_t v0, uint32_t v1, 
         "fma.rn.f32x2 ra, rv, rs, ra;\n\tmov.b64 {%0, %1}, ra;\n\t}"
         : "+f"(acc.x), "+f"(acc.y)
         : "r"(v0), "r"(v1), "f"(s0), "f"(s1));
-}
-
-// One output tile: weight rows [n0, n0 + 128) of group g, token rows [row0, row0 + rows).
-struct Tile {
-    int group, n_tile, row0, rows;
-};
-
-__device__ __forceinline__ Tile tile_at(int id, const ProductArgs &a, const int *first_tile, const int *offset, int bn)
-{
-    const int tt = id / a.n_tiles;
-    Tile t;
-    t.n_tile = id - tt * a.n_tiles;
-    int lo = 0, hi = a.groups;  // first_tile[lo] <= tt < first_tile[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (first_tile[mid] <= tt) lo = mid;
-        else hi = mid;
-    }
-    t.group = lo;
-    const int i = tt - first_tile[lo], parts = first_tile[lo + 1] - first_tile[lo];
-    const int r = offset[lo + 1] - offset[lo];
-    const int size = (((r + parts - 1) / parts) + 15) & ~15;  // <= bn
-    t.row0 = offset[lo] + i * size;
-    t.rows = min(size, offset[lo] + r - t.row0);  // may be <= 0 for the last part
-    return t;
 }
 
 template <class C, class OUT>
@@ -185,43 +132,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
         abort_flag = 0;
         fence_mbar_init();
     }
-    // groups: offsets clamped to an ascending sequence inside [0, rows], and each group's first token tile
-    if (!a.offsets) {
-        if (threadIdx.x == 0) {
-            offset[0] = 0;
-            offset[1] = a.rows;
-            first_tile[0] = 0;
-            first_tile[1] = (a.rows + C::BN - 1) / C::BN;
-        }
-    } else {
-        const int per = (a.groups + C::THREADS - 1) / C::THREADS;
-        const int g0 = min(a.groups, (int)threadIdx.x * per), g1 = min(a.groups, g0 + per);
-        int sum = 0;
-        for (int g = g0; g < g1; ++g) {
-            const int lo = min(max(__ldg(a.offsets + g), 0), a.rows);
-            const int hi = min(max(__ldg(a.offsets + g + 1), lo), a.rows);
-            offset[g] = lo;
-            if (g == a.groups - 1) offset[a.groups] = hi;
-            sum += (hi - lo + C::BN - 1) / C::BN;
-        }
-        int scan = sum;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, scan, d);
-            if (lane >= d) scan += v;
-        }
-        if (lane == 31) warp_tiles[warp] = scan;
-        __syncthreads();
-        int run = scan - sum;
-        for (int w = 0; w < warp; ++w) run += warp_tiles[w];
-        for (int g = g0; g < g1; ++g) {
-            first_tile[g] = run;
-            const int lo = offset[g];
-            const int hi = min(max(__ldg(a.offsets + g + 1), lo), a.rows);
-            run += (hi - lo + C::BN - 1) / C::BN;
-            if (g == a.groups - 1) first_tile[a.groups] = run;
-        }
-    }
+    build_groups<C::THREADS>(a, C::BN, offset, first_tile, warp_tiles);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -235,7 +146,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
     // roles skip their work but still meet at the cluster's barriers.
     int it = 0, sit = 0;  // this role's position in the operand ring / the block sequence
     for (int id = worker; id < n_work; id += workers) {
-        const Tile t = tile_at(id, a, first_tile, offset, C::BN);
+        const Tile t = tile_at(id, a.n_tiles, a.groups, first_tile, offset);
         const int ncols = (max(t.rows, 1) + 15) & ~15;
         float2 acc[C::COLS / 2];
         if (warp == C::EPI) {  // ---- TMA producer
@@ -280,17 +191,15 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
             const float *bs = a.b_scale + ((int64_t)t.group * a.n_tiles + t.n_tile) * a.kblocks;
             bool go = true;
             for (int k0 = kb0; k0 < kb1 && go; k0 += AHEAD) {
-                float v[AHEAD][PER];
+                // every load from a valid address, so that none waits behind a branch
+                float v[AHEAD][PER], w[AHEAD];
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i) {
-                    const float w = k0 + i < kb1 ? __ldg(bs + k0 + i) : 0.f;
+                    const int kb = min(k0 + i, kb1 - 1);
+                    w[i] = __ldg(bs + kb);
 #pragma unroll
-                    for (int j = 0; j < PER; ++j) {
-                        const int c = j * 32 + lane;
-                        v[i][j] = k0 + i < kb1 && c < t.rows
-                                      ? w * __ldg(a.a_scale + (int64_t)(k0 + i) * a.ld_a_scale + t.row0 + c)
-                                      : 0.f;
-                    }
+                    for (int j = 0; j < PER; ++j)
+                        v[i][j] = __ldg(a.a_scale + (int64_t)kb * a.ld_a_scale + t.row0 + min(j * 32 + lane, t.rows - 1));
                 }
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i) {
@@ -305,7 +214,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
                     if (!go) break;
 #pragma unroll
                     for (int j = 0; j < PER; ++j)
-                        if (j * 32 + lane < C::BN) scale_ring[s * C::BN + j * 32 + lane] = v[i][j];
+                        if (j * 32 + lane < C::BN) scale_ring[s * C::BN + j * 32 + lane] = v[i][j] * w[i];
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sc_full[s]);
                 }
@@ -367,8 +276,11 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
                 const int n = t.n_tile * kWeightRows + (threadIdx.x & 127);
                 for (int c = (int)rank * (C::EPI / 4) + (threadIdx.x >> 7); c < t.rows; c += ranks * (C::EPI / 4)) {
                     const uint32_t at = smem_u32(partial + c * kWeightRows + (threadIdx.x & 127));
-                    float v = 0.f;
-                    for (unsigned r = 0; r < ranks; ++r) v += cluster_ld_f32(cluster_map(at, r));
+                    float p[8], v = 0.f;
+#pragma unroll
+                    for (unsigned r = 0; r < 8; ++r) p[r] = r < ranks ? cluster_ld_f32(cluster_map(at, r)) : 0.f;
+#pragma unroll
+                    for (unsigned r = 0; r < 8; ++r) v += p[r];
                     if (n < a.n) static_cast<OUT *>(a.out)[(int64_t)(t.row0 + c) * a.ld_out + n] = OUT(v);
                 }
             }
@@ -398,27 +310,6 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
     if (warp == C::EPI + 1) tmem_dealloc(tmem, C::BUFS * C::BN);
 }
 
-// uint8 rows of `cols` codes, row stride ld bytes; boxes of 128 columns in the 128-byte swizzle
-bool code_map(CUtensorMap *m, const void *base, int cols, int64_t rows, int64_t ld, int64_t groups, int64_t stride,
-              int box_rows)
-{
-    const tmaps::EncodeTiledFn f = tmaps::encode_fn();
-    if (!f) return false;
-    const int dim = groups > 0 ? 3 : 2;
-    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)groups};
-    cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)stride};
-    cuuint32_t box[3] = {128, (cuuint32_t)box_rows, 1}, es[3] = {1, 1, 1};
-    return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, dim, const_cast<void *>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-struct Operands {
-    const uint8_t *a, *b;
-    int64_t ld_a, ld_b, stride_b;
-    int k;
-};
-
 template <class C>
 cudaError_t set_smem()
 {
@@ -447,7 +338,7 @@ cudaError_t product_prepare()
 {
     if (!tmaps::encode_fn()) return cudaErrorUnknown;
     const cudaError_t e = set_smem<Narrow>();
-    return e != cudaSuccess ? e : set_smem<Wide>();
+    return e != cudaSuccess ? e : pair_prepare();
 }
 
 moe_status product(const uint8_t *a, int64_t ld_a, const float *a_scale, int64_t ld_a_scale, int rows, const uint8_t *b,
@@ -490,9 +381,9 @@ moe_status product(const uint8_t *a, int64_t ld_a, const float *a_scale, int64_t
         return std::min<int64_t>(rows, used + (rows - used) / bn) * p.n_tiles;
     };
     if (most_tiles(Narrow::BN) > INT32_MAX) return MOE_ERR_INVALID_ARG;
-    const int64_t wide = most_tiles(Wide::BN);
-    const bool few_rows = (int64_t)rows <= 32ll * groups || wide < sms;
-    if (!few_rows) return run_product<Wide>(o, p, out_dtype, (int)std::min<int64_t>(wide, sms), 1, s);
+    const int64_t wide = most_tiles(kPairTokens) / p.n_tiles * ceil_div(n, 2 * kWeightRows);
+    const bool few_rows = (int64_t)rows <= 32ll * groups || wide < sms / 2;
+    if (!few_rows) return pair_product(o, p, out_dtype, (int)std::min<int64_t>(wide, sms / 2), s);
     const int64_t narrow = most_tiles(Narrow::BN);
     const int slots = 2 * sms;
     int ranks = 1;

@@ -1,0 +1,503 @@
+// The E4M3 product for many rows: a pair of CTAs (one cluster, two SMs of one
+// TPC) multiplies 256 weight rows by up to 256 token rows, 128 columns at a
+// time, with tcgen05.mma.cta_group::2.
+//
+// Each CTA brings 128 weight rows and half of the token rows, so a block of
+// 128 columns costs an SM 32 KB of operands for 512 clocks of tensor work (a
+// single CTA's 128 x 256 tile costs 48 KB, more than an SM gets from L2 in that
+// time).  The accumulator of CTA r holds weight rows 128 r .. 128 r + 127 (its
+// tensor-memory lanes) by all token columns, double buffered, one buffer per
+// block: the epilogue adds scale * partial to fp32 registers while the next
+// block is multiplied.
+//
+// The epilogue is the other bound: 128 x 256 fused multiply-adds a block and
+// CTA (256 clocks of the FMA pipes), and a token scale per column.  With one
+// weight row a thread would need all 128 scales of its half of the columns, and
+// shared memory returns 128 bytes a clock: 1024 clocks a block.  The 16 x 256-bit
+// tensor-memory load gives a thread 4 rows by a quarter of the columns instead,
+// two neighbouring columns in neighbouring registers, so 8 16-byte loads bring
+// its scales (256 clocks a block for the CTA) and a packed FMA serves two
+// columns.
+//
+// A thread's 4 rows are tensor-memory lanes r, r + 8, r + 16, r + 24 of its
+// warp's 32.  Where n is a multiple of 32 the weight rows are laid out by the
+// TMA box (rows 4 r + g at lane 8 g + r) such that they are 4 consecutive weight
+// rows: one 8-byte (bf16) or 16-byte (fp32) store a column, 8 lanes wide.
+//
+//   warps 0-7  epilogue: warpgroup h owns half h of the token columns
+//   warp 8     TMA producer (both CTAs; all bytes count on the leader's barrier)
+//   warp 9     MMA issuer (the leader's only)
+//   warps 10-11 scales a_scale * b_scale of each block, one half of the columns
+//              each, into a ring
+// Every mbarrier wait is bounded.
+#include "fp8_common.cuh"
+
+namespace moe {
+namespace fp8 {
+namespace {
+
+constexpr int kPairThreads = 384;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kScaleWarp0 = 10;
+constexpr int kPairStages = 6, kPairBufs = 2, kPairScales = 4;
+constexpr int kBox = 32;                                  // token rows of one TMA box
+constexpr int kPairStage = kABytes + (kPairTokens / 2) * 128;
+constexpr int kHalf = kPairTokens / 2;                    // columns of a warpgroup
+constexpr int kScaleStride = kHalf / 4 + 4;               // floats of a quarter of a half's scales, padded
+constexpr int kScaleRow = 4 * kScaleStride;               // one half's scales
+constexpr int kScaleAhead = 4;                            // blocks of scale loads in flight
+constexpr int kPairSmem = kPairStages * kPairStage + kPairScales * 2 * kScaleRow * 4 + 2 * (kMaxExperts + 1) * 4 + 1024;
+// registers: 384 threads at 168 are 256 at 216 and 128 at 72
+constexpr int kEpilogueRegs = 216, kOtherRegs = 72;
+static_assert(256 * kEpilogueRegs + 128 * kOtherRegs <= kPairThreads * 168, "register split exceeds the launch's");
+
+// ---- cta_group::2 forms ------------------------------------------------------------
+__device__ __forceinline__ void tmem_alloc2(uint32_t *dst, uint32_t ncols)
+{
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_relinquish2()
+{
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+__device__ __forceinline__ void mma2_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrive on `bar` of both CTAs once this thread's MMAs so far have completed.
+__device__ __forceinline__ void mma2_commit(uint64_t *bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// TMA loads into this CTA's shared memory whose bytes count on a barrier of either
+// CTA of the pair (a shared::cluster address).
+__device__ __forceinline__ void tma2_load_2d(void *dst, const void *tmap, uint32_t bar, int c0, int c1)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+        "%4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(tmap), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma2_load_3d(void *dst, const void *tmap, uint32_t bar, int c0, int c1, int c2)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+        "%4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(tmap), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma2_load_5d(void *dst, const void *tmap, uint32_t bar, int c0, int c1, int c2, int c3,
+                                             int c4)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+        "%4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(tmap), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+        : "memory");
+}
+
+// Arrive on a barrier of the pair (a shared::cluster address).  What it orders are
+// tensor-memory reads, complete and fenced before it (tcgen05.wait::ld,
+// fence::before_thread_sync): release and acquire at cluster scope, which order
+// all memory, cost 344 instead of 219 us on a 8192 x 4096 x 4096 product.
+__device__ __forceinline__ void pair_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// 32 columns of the warp's 32 lanes: v[4 i + 2 h + b] of group i (8 columns) are columns
+// 8 i + 2 (lane % 4) + b, rows lane / 4 + 8 h of lanes 0-15 (v) and 16-31 (w).
+struct Frag {
+    uint32_t v[16], w[16];
+};
+
+__device__ __forceinline__ void frag_request(uint32_t taddr, Frag &f)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(f.v[0]), "=r"(f.v[1]), "=r"(f.v[2]), "=r"(f.v[3]), "=r"(f.v[4]), "=r"(f.v[5]), "=r"(f.v[6]),
+          "=r"(f.v[7]), "=r"(f.v[8]), "=r"(f.v[9]), "=r"(f.v[10]), "=r"(f.v[11]), "=r"(f.v[12]), "=r"(f.v[13]),
+          "=r"(f.v[14]), "=r"(f.v[15])
+        : "r"(taddr));
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(f.w[0]), "=r"(f.w[1]), "=r"(f.w[2]), "=r"(f.w[3]), "=r"(f.w[4]), "=r"(f.w[5]), "=r"(f.w[6]),
+          "=r"(f.w[7]), "=r"(f.w[8]), "=r"(f.w[9]), "=r"(f.w[10]), "=r"(f.w[11]), "=r"(f.w[12]), "=r"(f.w[13]),
+          "=r"(f.w[14]), "=r"(f.w[15])
+        : "r"(taddr + (16u << 16)));
+}
+
+__device__ __forceinline__ void frag_wait(Frag &f)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(f.v[0]), "+r"(f.v[1]), "+r"(f.v[2]), "+r"(f.v[3]), "+r"(f.v[4]), "+r"(f.v[5]), "+r"(f.v[6]),
+                   "+r"(f.v[7]), "+r"(f.v[8]), "+r"(f.v[9]), "+r"(f.v[10]), "+r"(f.v[11]), "+r"(f.v[12]),
+                   "+r"(f.v[13]), "+r"(f.v[14]), "+r"(f.v[15]), "+r"(f.w[0]), "+r"(f.w[1]), "+r"(f.w[2]),
+                   "+r"(f.w[3]), "+r"(f.w[4]), "+r"(f.w[5]), "+r"(f.w[6]), "+r"(f.w[7]), "+r"(f.w[8]), "+r"(f.w[9]),
+                   "+r"(f.w[10]), "+r"(f.w[11]), "+r"(f.w[12]), "+r"(f.w[13]), "+r"(f.w[14]),
+                   "+r"(f.w[15])::"memory");
+}
+
+__device__ __forceinline__ void fma2(uint64_t &acc, uint32_t lo, uint32_t hi, uint64_t s)
+{
+    asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}"
+        : "+l"(acc)
+        : "r"(lo), "r"(hi), "l"(s));
+}
+
+__device__ __forceinline__ float pair_lo(uint64_t p) { return __uint_as_float((uint32_t)p); }
+__device__ __forceinline__ float pair_hi(uint64_t p) { return __uint_as_float((uint32_t)(p >> 32)); }
+
+__device__ __forceinline__ void store4(float *p, float a, float b, float c, float d)
+{
+    *reinterpret_cast<float4 *>(p) = make_float4(a, b, c, d);
+}
+
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, float a, float b, float c, float d)
+{
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(a, b), hi = __floats2bfloat162_rn(c, d);
+    *reinterpret_cast<uint2 *>(p) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+}
+
+// Token tile of the pair: column counts are multiples of 16 (tcgen05 N), the first
+// warpgroup's half a multiple of 32 (its load steps).
+struct Split {
+    int cols, first;  // all columns; columns of warpgroup 0
+};
+
+__device__ __forceinline__ Split split_columns(int rows)
+{
+    Split s;
+    s.cols = (rows + 15) & ~15;
+    s.first = min(s.cols, (((s.cols + 1) / 2) + 31) & ~31);
+    return s;
+}
+
+// PERM: weight rows permuted by the tensor map (n a multiple of 32), 4-wide stores.
+template <class OUT, bool PERM>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    fp8_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                    const ProductArgs a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t full[kPairStages], empty[kPairStages], acc_full[kPairBufs], acc_empty[kPairBufs],
+        sc_full[2 * kPairScales], sc_empty[2 * kPairScales], drain_bar;
+    __shared__ uint32_t tmem_base;
+    __shared__ int warp_tiles[kPairThreads / 32];
+    __shared__ volatile int abort_flag;
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float *scale_ring = reinterpret_cast<float *>(smem + kPairStages * kPairStage);  // [slot][half][kScaleRow]
+    int *offset = reinterpret_cast<int *>(scale_ring + kPairScales * 2 * kScaleRow);
+    int *first_tile = offset + kMaxExperts + 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned rank = cluster_rank();
+
+    if (warp == kMmaWarp) {
+        tmem_alloc2(&tmem_base, kPairBufs * kPairTokens);
+        tmem_relinquish2();
+    }
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPairStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < kPairBufs; ++s) {
+            mbar_init(&acc_full[s], 1);
+            mbar_init(&acc_empty[s], 16);  // the epilogue warps of both CTAs (used by the leader)
+        }
+        for (int s = 0; s < 2 * kPairScales; ++s) {
+            mbar_init(&sc_full[s], 1);
+            mbar_init(&sc_empty[s], 4);
+        }
+        mbar_init(&drain_bar, 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    build_groups<kPairThreads>(a, kPairTokens, offset, first_tile, warp_tiles);
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync();  // the other CTA's barriers and tensor memory exist from here on
+    tc_fence_after_sync();
+    const uint32_t tmem = tmem_base;
+    const int n_pairs = (a.n + 2 * kWeightRows - 1) / (2 * kWeightRows);
+    const int n_work = first_tile[a.groups] * n_pairs;
+    const int worker = blockIdx.x >> 1, workers = gridDim.x >> 1;
+
+    if (warp >= kTmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == kTmaWarp) {  // ---- TMA producer
+            if (lane == 0) {
+                prefetch_tmap(&map_w);
+                prefetch_tmap(&map_x);
+                int it = 0;
+                for (int id = worker; id < n_work && !abort_flag; id += workers) {
+                    const Tile t = tile_at(id, n_pairs, a.groups, first_tile, offset);
+                    const int mine = split_columns(t.rows).cols / 2;  // token rows of each CTA
+                    const int boxes = (mine + kBox - 1) / kBox;
+                    const int w0 = (t.n_tile * 2 + (int)rank) * kWeightRows, x0 = t.row0 + (int)rank * mine;
+                    for (int kb = 0; kb < a.kblocks; ++kb, ++it) {
+                        const int s = it % kPairStages, u = it / kPairStages;
+                        if (abort_flag || (u > 0 && !mbar_wait(&empty[s], (u - 1) & 1))) {
+                            abort_flag = 1;
+                            break;
+                        }
+                        uint8_t *w_s = smem + s * kPairStage, *x_s = w_s + kABytes;
+                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (kABytes + boxes * kBox * 128));
+                        const uint32_t bar = cluster_map(smem_u32(&full[s]), 0);
+                        if (PERM) tma2_load_5d(w_s, &map_w, bar, kb * 128, 0, 0, w0 / 32, t.group);
+                        else tma2_load_3d(w_s, &map_w, bar, kb * 128, w0, t.group);
+                        for (int b = 0; b < boxes; ++b)
+                            tma2_load_2d(x_s + b * kBox * 128, &map_x, bar, kb * 128, x0 + b * kBox);
+                    }
+                }
+                if (abort_flag && rank == 0) drain_ring(full, kPairStages, it);
+            }
+        } else if (warp == kMmaWarp) {  // ---- MMA issuer
+            if (lane == 0 && rank == 0) {
+                int it = 0;
+                for (int id = worker; id < n_work && !abort_flag; id += workers) {
+                    const Tile t = tile_at(id, n_pairs, a.groups, first_tile, offset);
+                    const uint32_t idesc = idesc_e4m3(2 * kWeightRows, split_columns(t.rows).cols);
+                    for (int kb = 0; kb < a.kblocks; ++kb, ++it) {
+                        const int s = it % kPairStages, u = it / kPairStages;
+                        const int d = it % kPairBufs, du = it / kPairBufs;
+                        if (abort_flag || (du > 0 && !mbar_wait(&acc_empty[d], (du - 1) & 1)) ||
+                            !mbar_wait(&full[s], u & 1)) {
+                            abort_flag = 1;
+                            break;
+                        }
+                        tc_fence_after_sync();
+                        const uint64_t wd = desc_kmajor_sw128(smem + s * kPairStage);
+                        const uint64_t xd = desc_kmajor_sw128(smem + s * kPairStage + kABytes);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma2_f8(tmem + d * kPairTokens, wd + 2 * kk, xd + 2 * kk, idesc, kk != 0);
+                        mma2_commit(&empty[s]);
+                        mma2_commit(&acc_full[d]);
+                    }
+                }
+                if (abort_flag) {
+                    mma2_commit(&drain_bar);
+                    mbar_wait(&drain_bar, 0);
+                }
+            }
+        } else {  // ---- scales of one half of the columns
+            const int half = warp - kScaleWarp0;
+            float *ring = scale_ring + half * kScaleRow;
+            int it = 0;
+            bool go = true;
+            for (int id = worker; id < n_work && go; id += workers) {
+                const Tile t = tile_at(id, n_pairs, a.groups, first_tile, offset);
+                const Split sp = split_columns(t.rows);
+                const int c0 = half ? sp.first : 0;
+                const int nb = t.n_tile * 2 + (int)rank;
+                const bool has_w = nb < a.n_tiles;
+                const float *bs = a.b_scale + ((int64_t)t.group * a.n_tiles + (has_w ? nb : 0)) * a.kblocks;
+                const float *as = a.a_scale + t.row0;
+                int at[4];  // this lane's columns, inside the tile
+#pragma unroll
+                for (int j = 0; j < 4; ++j) at[j] = min(c0 + j * 32 + lane, t.rows - 1);
+                for (int k0 = 0; k0 < a.kblocks && go; k0 += kScaleAhead) {
+                    // every load from a valid address, so that none waits behind a branch
+                    float v[kScaleAhead][4], w[kScaleAhead];
+#pragma unroll
+                    for (int i = 0; i < kScaleAhead; ++i) {
+                        const int kb = min(k0 + i, a.kblocks - 1);
+                        w[i] = __ldg(bs + kb);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[i][j] = __ldg(as + (int64_t)kb * a.ld_a_scale + at[j]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kScaleAhead; ++i) {
+                        if (k0 + i >= a.kblocks) break;
+                        const int s = it % kPairScales, u = it / kPairScales;
+                        ++it;
+                        if (lane == 0) {
+                            go = !abort_flag && (u == 0 || mbar_wait(&sc_empty[2 * s + half], (u - 1) & 1));
+                            if (!go) abort_flag = 1;
+                        }
+                        go = __shfl_sync(0xffffffffu, go, 0);
+                        if (!go) break;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int c = j * 32 + lane;
+                            ring[s * 2 * kScaleRow + ((c & 7) >> 1) * kScaleStride + (c >> 3) * 2 + (c & 1)] = has_w ? v[i][j] * w[i] : 0.f;
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sc_full[2 * s + half]);
+                    }
+                }
+            }
+        }
+    } else {  // ---- epilogue
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegs));
+        const int half = warp >> 2, quarter = warp & 3;
+        const uint32_t empty_at = cluster_map(smem_u32(acc_empty), 0);  // the leader's
+        int it = 0;
+        bool go = true;
+        for (int id = worker; id < n_work && go; id += workers) {
+            const Tile t = tile_at(id, n_pairs, a.groups, first_tile, offset);
+            const Split sp = split_columns(t.rows);
+            const int c0 = half ? sp.first : 0, cols = half ? sp.cols - sp.first : sp.first;
+            uint64_t acc[kHalf / 8][4];  // [column group][row group]: two columns
+#pragma unroll
+            for (int i = 0; i < kHalf / 8; ++i)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) acc[i][g] = 0;
+            for (int kb = 0; kb < a.kblocks; ++kb, ++it) {
+                const int d = it % kPairBufs, s = it % kPairScales;
+                go = !abort_flag && mbar_wait(&acc_full[d], (it / kPairBufs) & 1) &&
+                     mbar_wait(&sc_full[2 * s + half], (it / kPairScales) & 1);
+                go = __all_sync(0xffffffffu, go);
+                if (!go) {
+                    abort_flag = 1;
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint32_t td = tmem + d * kPairTokens + c0 + ((uint32_t)(quarter * 32) << 16);
+                const float *sc = scale_ring + (s * 2 + half) * kScaleRow + (lane & 3) * kScaleStride;
+                Frag f[2];
+                if (cols > 0) frag_request(td, f[0]);
+#pragma unroll
+                for (int i = 0; i < kHalf / 32; ++i) {
+                    if (32 * i < cols) {
+                        ulonglong2 w01 = *reinterpret_cast<const ulonglong2 *>(sc + 8 * i);
+                        ulonglong2 w23 = *reinterpret_cast<const ulonglong2 *>(sc + 8 * i + 4);
+                        frag_wait(f[i & 1]);
+                        if (32 * (i + 1) < cols) {
+                            frag_request(td + 32 * (i + 1), f[(i + 1) & 1]);
+                        } else {  // every value of the buffer has been read
+                            tc_fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) pair_arrive(empty_at + 8 * d);
+                        }
+                        const uint64_t w[4] = {w01.x, w01.y, w23.x, w23.y};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            fma2(acc[4 * i + q][0], f[i & 1].v[4 * q], f[i & 1].v[4 * q + 1], w[q]);
+                            fma2(acc[4 * i + q][1], f[i & 1].v[4 * q + 2], f[i & 1].v[4 * q + 3], w[q]);
+                            fma2(acc[4 * i + q][2], f[i & 1].w[4 * q], f[i & 1].w[4 * q + 1], w[q]);
+                            fma2(acc[4 * i + q][3], f[i & 1].w[4 * q + 2], f[i & 1].w[4 * q + 3], w[q]);
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    if (cols <= 0) pair_arrive(empty_at + 8 * d);
+                    mbar_arrive(&sc_empty[2 * s + half]);
+                }
+            }
+            if (!go) break;
+            const int n0 = (t.n_tile * 2 + (int)rank) * kWeightRows + quarter * 32;
+            const int first = c0 + 2 * (lane & 3);
+            OUT *out = static_cast<OUT *>(a.out) + (int64_t)(t.row0 + first) * a.ld_out;
+            if (PERM) {
+                const int n = n0 + 4 * (lane >> 2);
+                if (n < a.n) {
+#pragma unroll
+                    for (int i = 0; i < kHalf / 8; ++i) {
+                        if (8 * i >= cols) break;
+                        OUT *o = out + (int64_t)(8 * i) * a.ld_out + n;
+                        if (first + 8 * i < t.rows)
+                            store4(o, pair_lo(acc[i][0]), pair_lo(acc[i][1]), pair_lo(acc[i][2]), pair_lo(acc[i][3]));
+                        if (first + 8 * i + 1 < t.rows)
+                            store4(o + a.ld_out, pair_hi(acc[i][0]), pair_hi(acc[i][1]), pair_hi(acc[i][2]),
+                                   pair_hi(acc[i][3]));
+                    }
+                }
+            } else {
+                const int n = n0 + (lane >> 2);
+#pragma unroll
+                for (int i = 0; i < kHalf / 8; ++i) {
+                    if (8 * i >= cols) break;
+                    OUT *o = out + (int64_t)(8 * i) * a.ld_out + n;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        if (n + 8 * g >= a.n) break;
+                        if (first + 8 * i < t.rows) o[8 * g] = OUT(pair_lo(acc[i][g]));
+                        if (first + 8 * i + 1 < t.rows) o[a.ld_out + 8 * g] = OUT(pair_hi(acc[i][g]));
+                    }
+                }
+            }
+        }
+    }
+    __syncwarp();
+    if (abort_flag && threadIdx.x == 0 && a.status) atomicExch(a.status, (int)MOE_ERR_TIMEOUT);
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves while the other may still arrive here or read its operands
+    tc_fence_after_sync();
+    if (warp == kMmaWarp) tmem_dealloc2(tmem, kPairBufs * kPairTokens);
+}
+
+// Weight rows as [group][q][g][r][k] with row = 32 q + 4 r + g: a box of 128 rows puts
+// row 4 r + g of each 32 at shared-memory row 8 g + r.
+bool permuted_map(CUtensorMap *m, const Operands &o, const ProductArgs &a)
+{
+    const tmaps::EncodeTiledFn f = tmaps::encode_fn();
+    if (!f) return false;
+    cuuint64_t dims[5] = {(cuuint64_t)o.k, 8, 4, (cuuint64_t)(a.n / 32), (cuuint64_t)a.groups};
+    cuuint64_t strides[4] = {(cuuint64_t)o.ld_b * 4, (cuuint64_t)o.ld_b, (cuuint64_t)o.ld_b * 32, (cuuint64_t)o.stride_b};
+    cuuint32_t box[5] = {128, 8, 4, kWeightRows / 32, 1}, es[5] = {1, 1, 1, 1, 1};
+    return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<uint8_t *>(o.b), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class OUT>
+cudaError_t pair_launch(const CUtensorMap &mw, const CUtensorMap &mx, const ProductArgs &a, bool perm, int pairs,
+                        cudaStream_t s)
+{
+    return perm ? launch(fp8_pair_kernel<OUT, true>, dim3(2 * pairs), kPairThreads, kPairSmem, s, 2, false, mw, mx, a)
+                : launch(fp8_pair_kernel<OUT, false>, dim3(2 * pairs), kPairThreads, kPairSmem, s, 2, false, mw, mx, a);
+}
+
+}  // namespace
+
+cudaError_t pair_prepare()
+{
+    const cudaFuncAttribute smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    cudaError_t e = cudaFuncSetAttribute(fp8_pair_kernel<float, true>, smem, kPairSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fp8_pair_kernel<float, false>, smem, kPairSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fp8_pair_kernel<__nv_bfloat16, true>, smem, kPairSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fp8_pair_kernel<__nv_bfloat16, false>, smem, kPairSmem);
+    return e;
+}
+
+moe_status pair_product(const Operands &o, const ProductArgs &a, moe_dtype out_dtype, int pairs, cudaStream_t s)
+{
+    const bool bf16 = out_dtype == MOE_DT_BF16;
+    const bool perm = a.n % 32 == 0 && a.ld_out % 4 == 0 && aligned(a.out, bf16 ? 8 : 16);
+    CUtensorMap mw, mx;
+    if (perm ? !permuted_map(&mw, o, a) : !code_map(&mw, o.b, o.k, a.n, o.ld_b, a.groups, o.stride_b, kWeightRows))
+        return MOE_ERR_CUDA;
+    if (!code_map(&mx, o.a, o.k, a.rows, o.ld_a, 0, 0, kBox)) return MOE_ERR_CUDA;
+    return launched(bf16 ? pair_launch<__nv_bfloat16>(mw, mx, a, perm, pairs, s)
+                         : pair_launch<float>(mw, mx, a, perm, pairs, s));
+}
+
+}  // namespace fp8
+}  // namespace moe
