@@ -149,26 +149,16 @@ __device__ __forceinline__ void frag_request(uint32_t taddr, Frag &f)
         : "r"(taddr + (16u << 16)));
 }
 
-__device__ __forceinline__ void frag_wait(Frag &f)
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(f.v[0]), "+r"(f.v[1]), "+r"(f.v[2]), "+r"(f.v[3]), "+r"(f.v[4]), "+r"(f.v[5]), "+r"(f.v[6]),
-                   "+r"(f.v[7]), "+r"(f.v[8]), "+r"(f.v[9]), "+r"(f.v[10]), "+r"(f.v[11]), "+r"(f.v[12]),
-                   "+r"(f.v[13]), "+r"(f.v[14]), "+r"(f.v[15]), "+r"(f.w[0]), "+r"(f.w[1]), "+r"(f.w[2]),
-                   "+r"(f.w[3]), "+r"(f.w[4]), "+r"(f.w[5]), "+r"(f.w[6]), "+r"(f.w[7]), "+r"(f.w[8]), "+r"(f.w[9]),
-                   "+r"(f.w[10]), "+r"(f.w[11]), "+r"(f.w[12]), "+r"(f.w[13]), "+r"(f.w[14]),
-                   "+r"(f.w[15])::"memory");
-}
+// Waits for every request of this warp.  The fragment is not an operand: it would be
+// copied.  The FMAs that use it are volatile, so they stay behind the wait.
+__device__ __forceinline__ void frag_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void fma2(uint64_t &acc, uint32_t lo, uint32_t hi, uint64_t s)
+// Plain FMAs: the packed f32x2 form has the same rate (two a lane and two clocks), and
+// its operand pairs cost two moves each here (196 against 133 us below, epilogue alone).
+__device__ __forceinline__ void fma_volatile(float &acc, uint32_t v, float s)
 {
-    asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}"
-        : "+l"(acc)
-        : "r"(lo), "r"(hi), "l"(s));
+    asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(__uint_as_float(v)), "f"(s));
 }
-
-__device__ __forceinline__ float pair_lo(uint64_t p) { return __uint_as_float((uint32_t)p); }
-__device__ __forceinline__ float pair_hi(uint64_t p) { return __uint_as_float((uint32_t)(p >> 32)); }
 
 __device__ __forceinline__ void store4(float *p, float a, float b, float c, float d)
 {
@@ -194,6 +184,127 @@ __device__ __forceinline__ Split split_columns(int rows)
     s.cols = (rows + 15) & ~15;
     s.first = min(s.cols, (((s.cols + 1) / 2) + 31) & ~31);
     return s;
+}
+
+// ---- the epilogue --------------------------------------------------------------------
+// Shared memory by 32-bit addresses: the accumulators leave no registers for pointers.
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __noinline__ bool bar_wait(uint32_t bar, uint32_t parity)
+{
+    const long long t0 = clock64();
+    while (!bar_try(bar, parity))
+        if (clock64() - t0 > (1ll << 31)) return false;
+    return true;
+}
+
+__device__ __forceinline__ void bar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ float4 lds4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// What one warp needs of its CTA: barrier arrays, this half's scales at this lane's quarter
+// of the columns, this warp's tensor-memory lanes.
+struct Epilogue {
+    uint32_t acc_full, sc_full, sc_empty;  // sc_*: of this warp's half, every second barrier
+    uint32_t acc_empty;                    // the leader's (shared::cluster)
+    uint32_t tmem, scales;
+};
+
+// All blocks of a tile for 32 * STEPS columns from c0, then the stores.  The step
+// count is a template argument: with a branch per step the loads and FMAs of a
+// step cannot overlap (844 against 602 clocks a block, the loop alone).  False: a
+// wait ran out.
+template <int STEPS, class OUT, bool PERM>
+__device__ __forceinline__ bool epilogue_tile(const Epilogue &e, const ProductArgs &a, int c0, int rows, OUT *out,
+                                              int n_left, int &it)
+{
+    const int lane = threadIdx.x & 31;
+    float acc[4 * STEPS + 1][4][2];  // [column group][row group][column]
+#pragma unroll
+    for (int i = 0; i < 4 * STEPS; ++i)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) acc[i][g][0] = acc[i][g][1] = 0.f;
+    for (int kb = 0; kb < a.kblocks; ++kb, ++it) {
+        const int d = it % kPairBufs, s = it % kPairScales;
+        const uint32_t pa = (it / kPairBufs) & 1, ps = (it / kPairScales) & 1;
+        const bool sc_ready = bar_try(e.sc_full + 16 * s, ps), acc_ready = bar_try(e.acc_full + 8 * d, pa);
+        if (!__all_sync(0xffffffffu, sc_ready && acc_ready)) {
+            const bool ok = bar_wait(e.sc_full + 16 * s, ps) && bar_wait(e.acc_full + 8 * d, pa);
+            if (!__all_sync(0xffffffffu, ok)) return false;
+        }
+        tc_fence_after_sync();
+        const uint32_t td = e.tmem + d * kPairTokens + c0;
+        const uint32_t sc = e.scales + s * 2 * kScaleRow * 4;
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            Frag f;
+            frag_request(td + 32 * i, f);
+            const float4 w01 = lds4(sc + 32 * i), w23 = lds4(sc + 32 * i + 16);
+            frag_wait();
+            if (i == STEPS - 1) {  // every value of the buffer has been read
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) pair_arrive(e.acc_empty + 8 * d);
+            }
+            const float w[4][2] = {{w01.x, w01.y}, {w01.z, w01.w}, {w23.x, w23.y}, {w23.z, w23.w}};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    fma_volatile(acc[4 * i + q][0][b], f.v[4 * q + b], w[q][b]);
+                    fma_volatile(acc[4 * i + q][1][b], f.v[4 * q + 2 + b], w[q][b]);
+                    fma_volatile(acc[4 * i + q][2][b], f.w[4 * q + b], w[q][b]);
+                    fma_volatile(acc[4 * i + q][3][b], f.w[4 * q + 2 + b], w[q][b]);
+                }
+        }
+        __syncwarp();
+        if (lane == 0) {
+            if (STEPS == 0) pair_arrive(e.acc_empty + 8 * d);
+            bar_arrive(e.sc_empty + 16 * s);
+        }
+    }
+    // out: column c0 + 2 (lane % 4), this lane's first weight row, of which n_left are left
+    const int64_t group = 8 * a.ld_out;
+    int left = rows - c0 - 2 * (lane & 3);
+    if (n_left <= 0) return true;
+#pragma unroll
+    for (int i = 0; i < 4 * STEPS; ++i, out += group, left -= 8) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            OUT *o = b ? out + a.ld_out : out;
+            if (left <= b) continue;
+            if (PERM) {
+                store4(o, acc[i][0][b], acc[i][1][b], acc[i][2][b], acc[i][3][b]);
+            } else {
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    if (8 * g < n_left) o[8 * g] = OUT(acc[i][g][b]);
+            }
+        }
+    }
+    return true;
 }
 
 // PERM: weight rows permuted by the tensor map (n a multiple of 32), 4-wide stores.
@@ -260,7 +371,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     const int w0 = (t.n_tile * 2 + (int)rank) * kWeightRows, x0 = t.row0 + (int)rank * mine;
                     for (int kb = 0; kb < a.kblocks; ++kb, ++it) {
                         const int s = it % kPairStages, u = it / kPairStages;
-                        if (abort_flag || (u > 0 && !mbar_wait(&empty[s], (u - 1) & 1))) {
+                        if (u > 0 && !mbar_wait(&empty[s], (u - 1) & 1)) {
                             abort_flag = 1;
                             break;
                         }
@@ -284,8 +395,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     for (int kb = 0; kb < a.kblocks; ++kb, ++it) {
                         const int s = it % kPairStages, u = it / kPairStages;
                         const int d = it % kPairBufs, du = it / kPairBufs;
-                        if (abort_flag || (du > 0 && !mbar_wait(&acc_empty[d], (du - 1) & 1)) ||
-                            !mbar_wait(&full[s], u & 1)) {
+                        if (!mbar_wait(&full[s], u & 1) || (du > 0 && !mbar_wait(&acc_empty[d], (du - 1) & 1))) {
                             abort_flag = 1;
                             break;
                         }
@@ -336,7 +446,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         const int s = it % kPairScales, u = it / kPairScales;
                         ++it;
                         if (lane == 0) {
-                            go = !abort_flag && (u == 0 || mbar_wait(&sc_empty[2 * s + half], (u - 1) & 1));
+                            go = u == 0 || mbar_wait(&sc_empty[2 * s + half], (u - 1) & 1);
                             if (!go) abort_flag = 1;
                         }
                         go = __shfl_sync(0xffffffffu, go, 0);
@@ -355,93 +465,28 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     } else {  // ---- epilogue
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegs));
         const int half = warp >> 2, quarter = warp & 3;
-        const uint32_t empty_at = cluster_map(smem_u32(acc_empty), 0);  // the leader's
+        const Epilogue e{smem_u32(acc_full),
+                         smem_u32(sc_full + half),
+                         smem_u32(sc_empty + half),
+                         cluster_map(smem_u32(acc_empty), 0),
+                         tmem + ((uint32_t)(quarter * 32) << 16),
+                         smem_u32(scale_ring + half * kScaleRow + (lane & 3) * kScaleStride)};
         int it = 0;
         bool go = true;
         for (int id = worker; id < n_work && go; id += workers) {
             const Tile t = tile_at(id, n_pairs, a.groups, first_tile, offset);
             const Split sp = split_columns(t.rows);
             const int c0 = half ? sp.first : 0, cols = half ? sp.cols - sp.first : sp.first;
-            uint64_t acc[kHalf / 8][4];  // [column group][row group]: two columns
-#pragma unroll
-            for (int i = 0; i < kHalf / 8; ++i)
-#pragma unroll
-                for (int g = 0; g < 4; ++g) acc[i][g] = 0;
-            for (int kb = 0; kb < a.kblocks; ++kb, ++it) {
-                const int d = it % kPairBufs, s = it % kPairScales;
-                go = !abort_flag && mbar_wait(&acc_full[d], (it / kPairBufs) & 1) &&
-                     mbar_wait(&sc_full[2 * s + half], (it / kPairScales) & 1);
-                go = __all_sync(0xffffffffu, go);
-                if (!go) {
-                    abort_flag = 1;
-                    break;
-                }
-                tc_fence_after_sync();
-                const uint32_t td = tmem + d * kPairTokens + c0 + ((uint32_t)(quarter * 32) << 16);
-                const float *sc = scale_ring + (s * 2 + half) * kScaleRow + (lane & 3) * kScaleStride;
-                Frag f[2];
-                if (cols > 0) frag_request(td, f[0]);
-#pragma unroll
-                for (int i = 0; i < kHalf / 32; ++i) {
-                    if (32 * i < cols) {
-                        ulonglong2 w01 = *reinterpret_cast<const ulonglong2 *>(sc + 8 * i);
-                        ulonglong2 w23 = *reinterpret_cast<const ulonglong2 *>(sc + 8 * i + 4);
-                        frag_wait(f[i & 1]);
-                        if (32 * (i + 1) < cols) {
-                            frag_request(td + 32 * (i + 1), f[(i + 1) & 1]);
-                        } else {  // every value of the buffer has been read
-                            tc_fence_before_sync();
-                            __syncwarp();
-                            if (lane == 0) pair_arrive(empty_at + 8 * d);
-                        }
-                        const uint64_t w[4] = {w01.x, w01.y, w23.x, w23.y};
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            fma2(acc[4 * i + q][0], f[i & 1].v[4 * q], f[i & 1].v[4 * q + 1], w[q]);
-                            fma2(acc[4 * i + q][1], f[i & 1].v[4 * q + 2], f[i & 1].v[4 * q + 3], w[q]);
-                            fma2(acc[4 * i + q][2], f[i & 1].w[4 * q], f[i & 1].w[4 * q + 1], w[q]);
-                            fma2(acc[4 * i + q][3], f[i & 1].w[4 * q + 2], f[i & 1].w[4 * q + 3], w[q]);
-                        }
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) {
-                    if (cols <= 0) pair_arrive(empty_at + 8 * d);
-                    mbar_arrive(&sc_empty[2 * s + half]);
-                }
+            const int n = (t.n_tile * 2 + (int)rank) * kWeightRows + quarter * 32 + (PERM ? 4 : 1) * (lane >> 2);
+            OUT *out = static_cast<OUT *>(a.out) + (int64_t)(t.row0 + c0 + 2 * (lane & 3)) * a.ld_out + n;
+            switch ((cols + 31) / 32) {
+            case 0: go = epilogue_tile<0, OUT, PERM>(e, a, c0, t.rows, out, a.n - n, it); break;
+            case 1: go = epilogue_tile<1, OUT, PERM>(e, a, c0, t.rows, out, a.n - n, it); break;
+            case 2: go = epilogue_tile<2, OUT, PERM>(e, a, c0, t.rows, out, a.n - n, it); break;
+            case 3: go = epilogue_tile<3, OUT, PERM>(e, a, c0, t.rows, out, a.n - n, it); break;
+            default: go = epilogue_tile<4, OUT, PERM>(e, a, c0, t.rows, out, a.n - n, it); break;
             }
-            if (!go) break;
-            const int n0 = (t.n_tile * 2 + (int)rank) * kWeightRows + quarter * 32;
-            const int first = c0 + 2 * (lane & 3);
-            OUT *out = static_cast<OUT *>(a.out) + (int64_t)(t.row0 + first) * a.ld_out;
-            if (PERM) {
-                const int n = n0 + 4 * (lane >> 2);
-                if (n < a.n) {
-#pragma unroll
-                    for (int i = 0; i < kHalf / 8; ++i) {
-                        if (8 * i >= cols) break;
-                        OUT *o = out + (int64_t)(8 * i) * a.ld_out + n;
-                        if (first + 8 * i < t.rows)
-                            store4(o, pair_lo(acc[i][0]), pair_lo(acc[i][1]), pair_lo(acc[i][2]), pair_lo(acc[i][3]));
-                        if (first + 8 * i + 1 < t.rows)
-                            store4(o + a.ld_out, pair_hi(acc[i][0]), pair_hi(acc[i][1]), pair_hi(acc[i][2]),
-                                   pair_hi(acc[i][3]));
-                    }
-                }
-            } else {
-                const int n = n0 + (lane >> 2);
-#pragma unroll
-                for (int i = 0; i < kHalf / 8; ++i) {
-                    if (8 * i >= cols) break;
-                    OUT *o = out + (int64_t)(8 * i) * a.ld_out + n;
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        if (n + 8 * g >= a.n) break;
-                        if (first + 8 * i < t.rows) o[8 * g] = OUT(pair_lo(acc[i][g]));
-                        if (first + 8 * i + 1 < t.rows) o[a.ld_out + 8 * g] = OUT(pair_hi(acc[i][g]));
-                    }
-                }
-            }
+            if (!go) abort_flag = 1;
         }
     }
     __syncwarp();
