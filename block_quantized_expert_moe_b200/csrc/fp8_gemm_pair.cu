@@ -14,7 +14,7 @@
 // CTA (256 clocks of the FMA pipes), and a token scale per column.  With one
 // weight row a thread would need all 128 scales of its half of the columns, and
 // shared memory returns 128 bytes a clock: 1024 clocks a block.  The 16 x 256-bit
-// tensor-memory load gives a thread 4 rows by a quarter of the columns instead,
+// tensor-memory load gives a thread 4 rows by a quarter of its columns instead,
 // two neighbouring columns in neighbouring registers, so 8 16-byte loads bring
 // its scales (256 clocks a block for the CTA) and a packed FMA serves two
 // columns.
@@ -24,11 +24,11 @@
 // TMA box (rows 4 r + g at lane 8 g + r) such that they are 4 consecutive weight
 // rows: one 8-byte (bf16) or 16-byte (fp32) store a column, 8 lanes wide.
 //
-//   warps 0-7  epilogue: warpgroup h owns half h of the token columns
-//   warp 8     TMA producer (both CTAs; all bytes count on the leader's barrier)
-//   warp 9     MMA issuer (the leader's only)
-//   warps 10-11 scales a_scale * b_scale of each block, one half of the columns
-//              each, into a ring
+//   warps 0-15   epilogue: warpgroup q owns quarter q of the token columns
+//   warp 16      TMA producer (both CTAs; all bytes count on the leader's barrier)
+//   warp 17      MMA issuer (the leader's only)
+//   warps 18-19  scales a_scale * b_scale of each block, one half of the columns
+//                each, into a ring
 // Every mbarrier wait is bounded.
 #include "fp8_common.cuh"
 
@@ -36,19 +36,78 @@ namespace moe {
 namespace fp8 {
 namespace {
 
-constexpr int kPairThreads = 384;
-constexpr int kTmaWarp = 8, kMmaWarp = 9, kScaleWarp0 = 10;
+constexpr int kEpiWarps = 16;
+constexpr int kTmaWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1, kScaleWarp0 = kEpiWarps + 2;
+constexpr int kPairThreads = 32 * (kEpiWarps + 4);
 constexpr int kPairStages = 6, kPairBufs = 2, kPairScales = 4;
 constexpr int kBox = 32;                                  // token rows of one TMA box
 constexpr int kPairStage = kABytes + (kPairTokens / 2) * 128;
-constexpr int kHalf = kPairTokens / 2;                    // columns of a warpgroup
-constexpr int kScaleStride = kHalf / 4 + 4;               // floats of a quarter of a half's scales, padded
-constexpr int kScaleRow = 4 * kScaleStride;               // one half's scales
+constexpr int kScaleStride = kPairTokens / 4 + 4;         // floats of a quarter of a block's scales, padded
+constexpr int kScaleRow = 4 * kScaleStride;               // one block's scales
 constexpr int kScaleAhead = 4;                            // blocks of scale loads in flight
-constexpr int kPairSmem = kPairStages * kPairStage + kPairScales * 2 * kScaleRow * 4 + 2 * (kMaxExperts + 1) * 4 + 1024;
-// registers: 384 threads at 168 are 256 at 216 and 128 at 72
-constexpr int kEpilogueRegs = 216, kOtherRegs = 72;
-static_assert(256 * kEpilogueRegs + 128 * kOtherRegs <= kPairThreads * 168, "register split exceeds the launch's");
+constexpr int kPairSmem = kPairStages * kPairStage + kPairScales * kScaleRow * 4 + 2 * (kMaxExperts + 1) * 4 + 1024;
+// registers: 640 threads at 96 are 512 at 104 and 128 at 64
+constexpr int kEpilogueRegs = 104, kOtherRegs = 64;
+static_assert(32 * kEpiWarps * kEpilogueRegs + 128 * kOtherRegs <= kPairThreads * 96, "register split exceeds the launch's");
+
+// ---- shared memory by 32-bit addresses --------------------------------------------------
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity)
+{
+    const long long t0 = clock64();
+    while (!bar_try(bar, parity))
+        if (clock64() - t0 > (1ll << 31)) return false;
+    return true;
+}
+
+__device__ __forceinline__ void bar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ float4 lds4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
+// Position in a ring of N barriers: slot and the parity of its current use.
+template <int N>
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++slot == N) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
 
 // ---- cta_group::2 forms ------------------------------------------------------------
 __device__ __forceinline__ void tmem_alloc2(uint32_t *dst, uint32_t ncols)
@@ -79,11 +138,10 @@ __device__ __forceinline__ void mma2_f8(uint32_t d_tmem, uint64_t adesc, uint64_
 }
 
 // Arrive on `bar` of both CTAs once this thread's MMAs so far have completed.
-__device__ __forceinline__ void mma2_commit(uint64_t *bar)
+__device__ __forceinline__ void mma2_commit(uint32_t bar)
 {
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_u32(bar)),
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
         "h"((uint16_t)3)
         : "memory");
 }
@@ -127,26 +185,22 @@ __device__ __forceinline__ void pair_arrive(uint32_t bar)
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// 32 columns of the warp's 32 lanes: v[4 i + 2 h + b] of group i (8 columns) are columns
+// 16 columns of the warp's 32 lanes: v[4 i + 2 h + b] of group i (8 columns) are columns
 // 8 i + 2 (lane % 4) + b, rows lane / 4 + 8 h of lanes 0-15 (v) and 16-31 (w).
 struct Frag {
-    uint32_t v[16], w[16];
+    uint32_t v[8], w[8];
 };
 
 __device__ __forceinline__ void frag_request(uint32_t taddr, Frag &f)
 {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(f.v[0]), "=r"(f.v[1]), "=r"(f.v[2]), "=r"(f.v[3]), "=r"(f.v[4]), "=r"(f.v[5]), "=r"(f.v[6]),
-          "=r"(f.v[7]), "=r"(f.v[8]), "=r"(f.v[9]), "=r"(f.v[10]), "=r"(f.v[11]), "=r"(f.v[12]), "=r"(f.v[13]),
-          "=r"(f.v[14]), "=r"(f.v[15])
-        : "r"(taddr));
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(f.w[0]), "=r"(f.w[1]), "=r"(f.w[2]), "=r"(f.w[3]), "=r"(f.w[4]), "=r"(f.w[5]), "=r"(f.w[6]),
-          "=r"(f.w[7]), "=r"(f.w[8]), "=r"(f.w[9]), "=r"(f.w[10]), "=r"(f.w[11]), "=r"(f.w[12]), "=r"(f.w[13]),
-          "=r"(f.w[14]), "=r"(f.w[15])
-        : "r"(taddr + (16u << 16)));
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(f.v[0]), "=r"(f.v[1]), "=r"(f.v[2]), "=r"(f.v[3]), "=r"(f.v[4]), "=r"(f.v[5]), "=r"(f.v[6]),
+                   "=r"(f.v[7])
+                 : "r"(taddr));
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(f.w[0]), "=r"(f.w[1]), "=r"(f.w[2]), "=r"(f.w[3]), "=r"(f.w[4]), "=r"(f.w[5]), "=r"(f.w[6]),
+                   "=r"(f.w[7])
+                 : "r"(taddr + (16u << 16)));
 }
 
 // Waits for every request of this warp.  The fragment is not an operand: it would be
@@ -172,67 +226,20 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float a, float b, float
         make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
 }
 
-// Token tile of the pair: column counts are multiples of 16 (tcgen05 N), the first
-// warpgroup's half a multiple of 32 (its load steps).
-struct Split {
-    int cols, first;  // all columns; columns of warpgroup 0
-};
-
-__device__ __forceinline__ Split split_columns(int rows)
-{
-    Split s;
-    s.cols = (rows + 15) & ~15;
-    s.first = min(s.cols, (((s.cols + 1) / 2) + 31) & ~31);
-    return s;
-}
+// Columns of a pair's tile (tcgen05 N: a multiple of 16), and of each quarter of the epilogue warps
+__device__ __forceinline__ int tile_columns(int rows) { return (rows + 15) & ~15; }
+__device__ __forceinline__ int quarter_columns(int cols) { return ((cols + 3) / 4 + 15) & ~15; }
 
 // ---- the epilogue --------------------------------------------------------------------
-// Shared memory by 32-bit addresses: the accumulators leave no registers for pointers.
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-__device__ __noinline__ bool bar_wait(uint32_t bar, uint32_t parity)
-{
-    const long long t0 = clock64();
-    while (!bar_try(bar, parity))
-        if (clock64() - t0 > (1ll << 31)) return false;
-    return true;
-}
-
-__device__ __forceinline__ void bar_arrive(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ float4 lds4(uint32_t addr)
-{
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-
-// What one warp needs of its CTA: barrier arrays, this half's scales at this lane's quarter
-// of the columns, this warp's tensor-memory lanes.
+// What one warp needs of its CTA: barrier arrays, the scales of this lane's columns, this
+// warp's tensor-memory lanes.
 struct Epilogue {
-    uint32_t acc_full, sc_full, sc_empty;  // sc_*: of this warp's half, every second barrier
-    uint32_t acc_empty;                    // the leader's (shared::cluster)
+    uint32_t acc_full, sc_full, sc_empty;
+    uint32_t acc_empty;  // the leader's (shared::cluster)
     uint32_t tmem, scales;
 };
 
-// All blocks of a tile for 32 * STEPS columns from c0, then the stores.  The step
+// All blocks of a tile for 16 * STEPS columns from c0, then the stores.  The step
 // count is a template argument: with a branch per step the loads and FMAs of a
 // step cannot overlap (844 against 602 clocks a block, the loop alone).  False: a
 // wait ran out.
@@ -241,48 +248,48 @@ __device__ __forceinline__ bool epilogue_tile(const Epilogue &e, const ProductAr
                                               int n_left, int &it)
 {
     const int lane = threadIdx.x & 31;
-    float acc[4 * STEPS + 1][4][2];  // [column group][row group][column]
+    float acc[2 * STEPS + 1][4][2];  // [column group][row group][column]
 #pragma unroll
-    for (int i = 0; i < 4 * STEPS; ++i)
+    for (int i = 0; i < 2 * STEPS; ++i)
 #pragma unroll
         for (int g = 0; g < 4; ++g) acc[i][g][0] = acc[i][g][1] = 0.f;
     for (int kb = 0; kb < a.kblocks; ++kb, ++it) {
         const int d = it % kPairBufs, s = it % kPairScales;
         const uint32_t pa = (it / kPairBufs) & 1, ps = (it / kPairScales) & 1;
-        const bool sc_ready = bar_try(e.sc_full + 16 * s, ps), acc_ready = bar_try(e.acc_full + 8 * d, pa);
+        const bool sc_ready = bar_try(e.sc_full + 8 * s, ps), acc_ready = bar_try(e.acc_full + 8 * d, pa);
         if (!__all_sync(0xffffffffu, sc_ready && acc_ready)) {
-            const bool ok = bar_wait(e.sc_full + 16 * s, ps) && bar_wait(e.acc_full + 8 * d, pa);
+            const bool ok = bar_wait(e.sc_full + 8 * s, ps) && bar_wait(e.acc_full + 8 * d, pa);
             if (!__all_sync(0xffffffffu, ok)) return false;
         }
         tc_fence_after_sync();
         const uint32_t td = e.tmem + d * kPairTokens + c0;
-        const uint32_t sc = e.scales + s * 2 * kScaleRow * 4;
+        const uint32_t sc = e.scales + (s * kScaleRow + c0 / 4) * 4;
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
             Frag f;
-            frag_request(td + 32 * i, f);
-            const float4 w01 = lds4(sc + 32 * i), w23 = lds4(sc + 32 * i + 16);
+            frag_request(td + 16 * i, f);
+            const float4 w4 = lds4(sc + 16 * i);
             frag_wait();
             if (i == STEPS - 1) {  // every value of the buffer has been read
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) pair_arrive(e.acc_empty + 8 * d);
             }
-            const float w[4][2] = {{w01.x, w01.y}, {w01.z, w01.w}, {w23.x, w23.y}, {w23.z, w23.w}};
+            const float w[2][2] = {{w4.x, w4.y}, {w4.z, w4.w}};
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    fma_volatile(acc[4 * i + q][0][b], f.v[4 * q + b], w[q][b]);
-                    fma_volatile(acc[4 * i + q][1][b], f.v[4 * q + 2 + b], w[q][b]);
-                    fma_volatile(acc[4 * i + q][2][b], f.w[4 * q + b], w[q][b]);
-                    fma_volatile(acc[4 * i + q][3][b], f.w[4 * q + 2 + b], w[q][b]);
+                    fma_volatile(acc[2 * i + q][0][b], f.v[4 * q + b], w[q][b]);
+                    fma_volatile(acc[2 * i + q][1][b], f.v[4 * q + 2 + b], w[q][b]);
+                    fma_volatile(acc[2 * i + q][2][b], f.w[4 * q + b], w[q][b]);
+                    fma_volatile(acc[2 * i + q][3][b], f.w[4 * q + 2 + b], w[q][b]);
                 }
         }
         __syncwarp();
         if (lane == 0) {
             if (STEPS == 0) pair_arrive(e.acc_empty + 8 * d);
-            bar_arrive(e.sc_empty + 16 * s);
+            bar_arrive(e.sc_empty + 8 * s);
         }
     }
     // out: column c0 + 2 (lane % 4), this lane's first weight row, of which n_left are left
@@ -290,7 +297,7 @@ __device__ __forceinline__ bool epilogue_tile(const Epilogue &e, const ProductAr
     int left = rows - c0 - 2 * (lane & 3);
     if (n_left <= 0) return true;
 #pragma unroll
-    for (int i = 0; i < 4 * STEPS; ++i, out += group, left -= 8) {
+    for (int i = 0; i < 2 * STEPS; ++i, out += group, left -= 8) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             OUT *o = b ? out + a.ld_out : out;
@@ -315,13 +322,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 {
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[kPairStages], empty[kPairStages], acc_full[kPairBufs], acc_empty[kPairBufs],
-        sc_full[2 * kPairScales], sc_empty[2 * kPairScales], drain_bar;
+        sc_full[kPairScales], sc_empty[kPairScales], drain_bar;
     __shared__ uint32_t tmem_base;
     __shared__ int warp_tiles[kPairThreads / 32];
     __shared__ volatile int abort_flag;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float *scale_ring = reinterpret_cast<float *>(smem + kPairStages * kPairStage);  // [slot][half][kScaleRow]
-    int *offset = reinterpret_cast<int *>(scale_ring + kPairScales * 2 * kScaleRow);
+    float *scale_ring = reinterpret_cast<float *>(smem + kPairStages * kPairStage);  // [slot][kScaleRow]
+    int *offset = reinterpret_cast<int *>(scale_ring + kPairScales * kScaleRow);
     int *first_tile = offset + kMaxExperts + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned rank = cluster_rank();
@@ -337,11 +344,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         for (int s = 0; s < kPairBufs; ++s) {
             mbar_init(&acc_full[s], 1);
-            mbar_init(&acc_empty[s], 16);  // the epilogue warps of both CTAs (used by the leader)
+            mbar_init(&acc_empty[s], 2 * kEpiWarps);  // the epilogue warps of both CTAs (used by the leader)
         }
-        for (int s = 0; s < 2 * kPairScales; ++s) {
-            mbar_init(&sc_full[s], 1);
-            mbar_init(&sc_empty[s], 4);
+        for (int s = 0; s < kPairScales; ++s) {
+            mbar_init(&sc_full[s], 2);
+            mbar_init(&sc_empty[s], kEpiWarps);
         }
         mbar_init(&drain_bar, 1);
         abort_flag = 0;
@@ -363,66 +370,84 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             if (lane == 0) {
                 prefetch_tmap(&map_w);
                 prefetch_tmap(&map_x);
-                int it = 0;
-                for (int id = worker; id < n_work && !abort_flag; id += workers) {
-                    const Tile t = tile_at(id, n_pairs, a.groups, first_tile, offset);
-                    const int mine = split_columns(t.rows).cols / 2;  // token rows of each CTA
-                    const int boxes = (mine + kBox - 1) / kBox;
-                    const int w0 = (t.n_tile * 2 + (int)rank) * kWeightRows, x0 = t.row0 + (int)rank * mine;
-                    for (int kb = 0; kb < a.kblocks; ++kb, ++it) {
-                        const int s = it % kPairStages, u = it / kPairStages;
-                        if (u > 0 && !mbar_wait(&empty[s], (u - 1) & 1)) {
-                            abort_flag = 1;
-                            break;
-                        }
-                        uint8_t *w_s = smem + s * kPairStage, *x_s = w_s + kABytes;
-                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (kABytes + boxes * kBox * 128));
-                        const uint32_t bar = cluster_map(smem_u32(&full[s]), 0);
+            }
+            const uint32_t full_at = smem_u32(full), empty_at = smem_u32(empty), leader_full = cluster_map(full_at, 0);
+            Ring<kPairStages> r;
+            int issued = 0;
+            bool go = true;
+            for (int id = worker; id < n_work && go; id += workers) {
+                const Tile t = tile_at(id, n_pairs, a.groups, first_tile, offset);
+                const int mine = tile_columns(t.rows) / 2;  // token rows of each CTA
+                const int boxes = (mine + kBox - 1) / kBox;
+                const uint32_t bytes = 2 * (kABytes + boxes * kBox * 128);
+                const int w0 = (t.n_tile * 2 + (int)rank) * kWeightRows, x0 = t.row0 + (int)rank * mine;
+                for (int kb = 0; kb < a.kblocks; ++kb, ++issued, r.next()) {
+                    // the slot's previous use has been multiplied (a fresh slot passes)
+                    if (!__all_sync(0xffffffffu, bar_wait(empty_at + 8 * r.slot, r.phase ^ 1))) {
+                        go = false;
+                        break;
+                    }
+                    if (elect_one()) {
+                        uint8_t *w_s = smem + r.slot * kPairStage, *x_s = w_s + kABytes;
+                        if (rank == 0) mbar_arrive_expect_tx(&full[r.slot], bytes);
+                        const uint32_t bar = leader_full + 8 * r.slot;
                         if (PERM) tma2_load_5d(w_s, &map_w, bar, kb * 128, 0, 0, w0 / 32, t.group);
                         else tma2_load_3d(w_s, &map_w, bar, kb * 128, w0, t.group);
                         for (int b = 0; b < boxes; ++b)
                             tma2_load_2d(x_s + b * kBox * 128, &map_x, bar, kb * 128, x0 + b * kBox);
                     }
+                    __syncwarp();
                 }
-                if (abort_flag && rank == 0) drain_ring(full, kPairStages, it);
+            }
+            if (!go) {
+                if (lane == 0) abort_flag = 1;
+                if (rank == 0 && lane == 0) drain_ring(full, kPairStages, issued);
             }
         } else if (warp == kMmaWarp) {  // ---- MMA issuer
-            if (lane == 0 && rank == 0) {
-                int it = 0;
-                for (int id = worker; id < n_work && !abort_flag; id += workers) {
+            // the whole warp runs the loop and one lane issues: in a branch of one lane the
+            // descriptors do not count as uniform, and each instruction costs a sequence of moves
+            if (rank == 0) {
+                const uint32_t full_at = smem_u32(full), empty_at = smem_u32(empty), acc_full_at = smem_u32(acc_full),
+                               acc_empty_at = smem_u32(acc_empty);
+                const uint64_t w_desc = desc_kmajor_sw128(smem), x_desc = desc_kmajor_sw128(smem + kABytes);
+                Ring<kPairStages> r;
+                Ring<kPairBufs> d;
+                bool go = true;
+                for (int id = worker; id < n_work && go; id += workers) {
                     const Tile t = tile_at(id, n_pairs, a.groups, first_tile, offset);
-                    const uint32_t idesc = idesc_e4m3(2 * kWeightRows, split_columns(t.rows).cols);
-                    for (int kb = 0; kb < a.kblocks; ++kb, ++it) {
-                        const int s = it % kPairStages, u = it / kPairStages;
-                        const int d = it % kPairBufs, du = it / kPairBufs;
-                        if (!mbar_wait(&full[s], u & 1) || (du > 0 && !mbar_wait(&acc_empty[d], (du - 1) & 1))) {
-                            abort_flag = 1;
+                    const uint32_t idesc = idesc_e4m3(2 * kWeightRows, tile_columns(t.rows));
+                    for (int kb = 0; kb < a.kblocks; ++kb, r.next(), d.next()) {
+                        const bool ok = bar_wait(full_at + 8 * r.slot, r.phase) &&
+                                        bar_wait(acc_empty_at + 8 * d.slot, d.phase ^ 1);
+                        if (!__all_sync(0xffffffffu, ok)) {
+                            go = false;
                             break;
                         }
                         tc_fence_after_sync();
-                        const uint64_t wd = desc_kmajor_sw128(smem + s * kPairStage);
-                        const uint64_t xd = desc_kmajor_sw128(smem + s * kPairStage + kABytes);
+                        if (elect_one()) {
+                            const uint64_t step = (uint64_t)(r.slot * (kPairStage >> 4));
+                            const uint64_t wd = w_desc + step, xd = x_desc + step;
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma2_f8(tmem + d * kPairTokens, wd + 2 * kk, xd + 2 * kk, idesc, kk != 0);
-                        mma2_commit(&empty[s]);
-                        mma2_commit(&acc_full[d]);
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma2_f8(tmem + d.slot * kPairTokens, wd + 2 * kk, xd + 2 * kk, idesc, kk != 0);
+                            mma2_commit(empty_at + 8 * r.slot);
+                            mma2_commit(acc_full_at + 8 * d.slot);
+                        }
+                        __syncwarp();
                     }
                 }
-                if (abort_flag) {
-                    mma2_commit(&drain_bar);
+                if (!go && elect_one()) {
+                    abort_flag = 1;
+                    mma2_commit(smem_u32(&drain_bar));
                     mbar_wait(&drain_bar, 0);
                 }
             }
-        } else {  // ---- scales of one half of the columns
-            const int half = warp - kScaleWarp0;
-            float *ring = scale_ring + half * kScaleRow;
+        } else {  // ---- scales of half of the columns
+            const int c0 = (warp - kScaleWarp0) * (kPairTokens / 2);
             int it = 0;
             bool go = true;
             for (int id = worker; id < n_work && go; id += workers) {
                 const Tile t = tile_at(id, n_pairs, a.groups, first_tile, offset);
-                const Split sp = split_columns(t.rows);
-                const int c0 = half ? sp.first : 0;
                 const int nb = t.n_tile * 2 + (int)rank;
                 const bool has_w = nb < a.n_tiles;
                 const float *bs = a.b_scale + ((int64_t)t.group * a.n_tiles + (has_w ? nb : 0)) * a.kblocks;
@@ -446,40 +471,40 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         const int s = it % kPairScales, u = it / kPairScales;
                         ++it;
                         if (lane == 0) {
-                            go = u == 0 || mbar_wait(&sc_empty[2 * s + half], (u - 1) & 1);
+                            go = u == 0 || mbar_wait(&sc_empty[s], (u - 1) & 1);
                             if (!go) abort_flag = 1;
                         }
                         go = __shfl_sync(0xffffffffu, go, 0);
                         if (!go) break;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const int c = j * 32 + lane;
-                            ring[s * 2 * kScaleRow + ((c & 7) >> 1) * kScaleStride + (c >> 3) * 2 + (c & 1)] = has_w ? v[i][j] * w[i] : 0.f;
+                            const int c = c0 + j * 32 + lane;
+                            scale_ring[s * kScaleRow + ((c & 7) >> 1) * kScaleStride + (c >> 3) * 2 + (c & 1)] = has_w ? v[i][j] * w[i] : 0.f;
                         }
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&sc_full[2 * s + half]);
+                        if (lane == 0) mbar_arrive(&sc_full[s]);
                     }
                 }
             }
         }
     } else {  // ---- epilogue
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegs));
-        const int half = warp >> 2, quarter = warp & 3;
+        const int part = warp >> 2, quarter = warp & 3;
         const Epilogue e{smem_u32(acc_full),
-                         smem_u32(sc_full + half),
-                         smem_u32(sc_empty + half),
+                         smem_u32(sc_full),
+                         smem_u32(sc_empty),
                          cluster_map(smem_u32(acc_empty), 0),
                          tmem + ((uint32_t)(quarter * 32) << 16),
-                         smem_u32(scale_ring + half * kScaleRow + (lane & 3) * kScaleStride)};
+                         smem_u32(scale_ring + (lane & 3) * kScaleStride)};
         int it = 0;
         bool go = true;
         for (int id = worker; id < n_work && go; id += workers) {
             const Tile t = tile_at(id, n_pairs, a.groups, first_tile, offset);
-            const Split sp = split_columns(t.rows);
-            const int c0 = half ? sp.first : 0, cols = half ? sp.cols - sp.first : sp.first;
+            const int all = tile_columns(t.rows), most = quarter_columns(all);
+            const int c0 = min(part * most, all), cols = min(most, all - c0);
             const int n = (t.n_tile * 2 + (int)rank) * kWeightRows + quarter * 32 + (PERM ? 4 : 1) * (lane >> 2);
             OUT *out = static_cast<OUT *>(a.out) + (int64_t)(t.row0 + c0 + 2 * (lane & 3)) * a.ld_out + n;
-            switch ((cols + 31) / 32) {
+            switch (cols / 16) {
             case 0: go = epilogue_tile<0, OUT, PERM>(e, a, c0, t.rows, out, a.n - n, it); break;
             case 1: go = epilogue_tile<1, OUT, PERM>(e, a, c0, t.rows, out, a.n - n, it); break;
             case 2: go = epilogue_tile<2, OUT, PERM>(e, a, c0, t.rows, out, a.n - n, it); break;
