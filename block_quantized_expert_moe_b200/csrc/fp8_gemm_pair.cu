@@ -1,34 +1,28 @@
 // The E4M3 product for many rows: a pair of CTAs (one cluster, two SMs of one
-// TPC) multiplies 256 weight rows by up to 256 token rows, 128 columns at a
-// time, with tcgen05.mma.cta_group::2.
+// TPC) multiplies up to 256 token rows by 256 weight rows, 128 columns at a time,
+// with tcgen05.mma.cta_group::2.
 //
-// Each CTA brings 128 weight rows and half of the token rows, so a block of
+// Each CTA brings up to 128 token rows and half of the weight rows, so a block of
 // 128 columns costs an SM 32 KB of operands for 512 clocks of tensor work (a
 // single CTA's 128 x 256 tile costs 48 KB, more than an SM gets from L2 in that
-// time).  The accumulator of CTA r holds weight rows 128 r .. 128 r + 127 (its
-// tensor-memory lanes) by all token columns, double buffered, one buffer per
-// block: the epilogue adds scale * partial to fp32 registers while the next
-// block is multiplied.
+// time).  A CTA's accumulator holds its token rows (tensor-memory lanes) by all
+// 256 weight rows, double buffered, one buffer per block: the epilogue adds scale *
+// partial to fp32 registers while the next block is multiplied.  A group's last
+// tile is cut in half between the two CTAs, so its empty lanes are whole warps of
+// the epilogue, which skip.
 //
-// The epilogue is the other bound: 128 x 256 fused multiply-adds a block and
-// CTA (256 clocks of the FMA pipes), and a token scale per column.  With one
-// weight row a thread would need all 128 scales of its half of the columns, and
-// shared memory returns 128 bytes a clock: 1024 clocks a block.  The 16 x 256-bit
-// tensor-memory load gives a thread 4 rows by a quarter of its columns instead,
-// two neighbouring columns in neighbouring registers, so 8 16-byte loads bring
-// its scales (256 clocks a block for the CTA) and a packed FMA serves two
-// columns.
+// The epilogue is the other bound: 128 x 256 fused multiply-adds a block and CTA,
+// 256 clocks of the FMA pipes.  Tokens on the lanes give a thread one row: its scale is
+// one register, loaded two blocks ahead, and one product with the weights' block
+// scale covers all its columns.  (With the weights on the lanes, as in the kernel
+// for few rows, every column has a scale of its own, read from shared memory:
+// 153.7 us at 8192 x 4096 x 4096.)  Sixteen warps, four per scheduler, hide the barrier
+// and tensor-memory latencies of one another.
 //
-// A thread's 4 rows are tensor-memory lanes r, r + 8, r + 16, r + 24 of its
-// warp's 32.  Where n is a multiple of 32 the weight rows are laid out by the
-// TMA box (rows 4 r + g at lane 8 g + r) such that they are 4 consecutive weight
-// rows: one 8-byte (bf16) or 16-byte (fp32) store a column, 8 lanes wide.
-//
-//   warps 0-15   epilogue: warpgroup q owns quarter q of the token columns
+//   warps 0-15   epilogue: warpgroup q owns columns 64 q .. 64 q + 63
 //   warp 16      TMA producer (both CTAs; all bytes count on the leader's barrier)
 //   warp 17      MMA issuer (the leader's only)
-//   warps 18-19  scales a_scale * b_scale of each block, one half of the columns
-//                each, into a ring
+//   warps 18-19  idle (a register split works on groups of four warps)
 // Every mbarrier wait is bounded.
 #include "fp8_common.cuh"
 
@@ -37,17 +31,16 @@ namespace fp8 {
 namespace {
 
 constexpr int kEpiWarps = 16;
-constexpr int kTmaWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1, kScaleWarp0 = kEpiWarps + 2;
+constexpr int kTmaWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
 constexpr int kPairThreads = 32 * (kEpiWarps + 4);
-constexpr int kPairStages = 6, kPairBufs = 2, kPairScales = 4;
-constexpr int kBox = 32;                                  // token rows of one TMA box
-constexpr int kPairStage = kABytes + (kPairTokens / 2) * 128;
-constexpr int kScaleStride = kPairTokens / 4 + 4;         // floats of a quarter of a block's scales, padded
-constexpr int kScaleRow = 4 * kScaleStride;               // one block's scales
-constexpr int kScaleAhead = 4;                            // blocks of scale loads in flight
-constexpr int kPairSmem = kPairStages * kPairStage + kPairScales * kScaleRow * 4 + 2 * (kMaxExperts + 1) * 4 + 1024;
-// registers: 640 threads at 96 are 512 at 104 and 128 at 64
-constexpr int kEpilogueRegs = 104, kOtherRegs = 64;
+constexpr int kPairStages = 6, kPairBufs = 2;
+constexpr int kPairWeights = 256;          // weight rows (accumulator columns) of a tile
+constexpr int kPart = kPairWeights / 4;    // columns of a warpgroup
+constexpr int kBox = 32;                   // token rows of one TMA box
+constexpr int kPairStage = 2 * kABytes;    // 128 token rows, 128 weight rows
+constexpr int kPairSmem = kPairStages * kPairStage + 2 * (kMaxExperts + 1) * 4 + 1024;
+// registers: 640 threads at 96 are 512 at 112 and 128 at 32
+constexpr int kEpilogueRegs = 112, kOtherRegs = 32;
 static_assert(32 * kEpiWarps * kEpilogueRegs + 128 * kOtherRegs <= kPairThreads * 96, "register split exceeds the launch's");
 
 // ---- shared memory by 32-bit addresses --------------------------------------------------
@@ -66,25 +59,11 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
 
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity)
 {
+    if (bar_try(bar, parity)) return true;
     const long long t0 = clock64();
     while (!bar_try(bar, parity))
         if (clock64() - t0 > (1ll << 31)) return false;
     return true;
-}
-
-__device__ __forceinline__ void bar_arrive(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ float4 lds4(uint32_t addr)
-{
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
 }
 
 // One lane of a converged warp.
@@ -166,16 +145,6 @@ __device__ __forceinline__ void tma2_load_3d(void *dst, const void *tmap, uint32
         : "memory");
 }
 
-__device__ __forceinline__ void tma2_load_5d(void *dst, const void *tmap, uint32_t bar, int c0, int c1, int c2, int c3,
-                                             int c4)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
-        "%4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(tmap), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
-        : "memory");
-}
-
 // Arrive on a barrier of the pair (a shared::cluster address).  What it orders are
 // tensor-memory reads, complete and fenced before it (tcgen05.wait::ld,
 // fence::before_thread_sync): release and acquire at cluster scope, which order
@@ -185,156 +154,108 @@ __device__ __forceinline__ void pair_arrive(uint32_t bar)
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// 16 columns of the warp's 32 lanes: v[4 i + 2 h + b] of group i (8 columns) are columns
-// 8 i + 2 (lane % 4) + b, rows lane / 4 + 8 h of lanes 0-15 (v) and 16-31 (w).
-struct Frag {
-    uint32_t v[8], w[8];
-};
-
-__device__ __forceinline__ void frag_request(uint32_t taddr, Frag &f)
+// 16 columns of this thread's lane; valid after columns_wait.  They are no operands of the
+// wait (they would be copied); the FMAs that use them are volatile and stay behind it.
+// (32 at a time leave too few registers: spilled loop variables cost 1000 clocks a turn.)
+constexpr int kStep = 16;
+__device__ __forceinline__ void columns_request(uint32_t taddr, uint32_t (&v)[kStep])
 {
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(f.v[0]), "=r"(f.v[1]), "=r"(f.v[2]), "=r"(f.v[3]), "=r"(f.v[4]), "=r"(f.v[5]), "=r"(f.v[6]),
-                   "=r"(f.v[7])
-                 : "r"(taddr));
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(f.w[0]), "=r"(f.w[1]), "=r"(f.w[2]), "=r"(f.w[3]), "=r"(f.w[4]), "=r"(f.w[5]), "=r"(f.w[6]),
-                   "=r"(f.w[7])
-                 : "r"(taddr + (16u << 16)));
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
 }
 
-// Waits for every request of this warp.  The fragment is not an operand: it would be
-// copied.  The FMAs that use it are volatile, so they stay behind the wait.
-__device__ __forceinline__ void frag_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void columns_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// Plain FMAs: the packed f32x2 form has the same rate (two a lane and two clocks), and
-// its operand pairs cost two moves each here (196 against 133 us below, epilogue alone).
+// Volatile, so that the load stays where it is written, ahead of the blocks whose time hides it.
+__device__ __forceinline__ float load_ahead(const float *p)
+{
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+
+// Plain FMAs: the packed f32x2 form has the same rate, and its operand pairs cost moves
+// (650 against 601 clocks a block of 256 columns, the loop alone).
 __device__ __forceinline__ void fma_volatile(float &acc, uint32_t v, float s)
 {
     asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(__uint_as_float(v)), "f"(s));
 }
 
-__device__ __forceinline__ void store4(float *p, float a, float b, float c, float d)
+// 32 bytes (a whole sector) of one output row
+__device__ __forceinline__ void store_sector(void *p, const uint32_t (&w)[8])
 {
-    *reinterpret_cast<float4 *>(p) = make_float4(a, b, c, d);
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
 }
 
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, float a, float b, float c, float d)
+// `left` columns (of 64) of one row; WIDE: the row starts on 32 bytes.
+template <bool WIDE>
+__device__ __forceinline__ void store_row(float *out, const float (&acc)[kPart], int left)
 {
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(a, b), hi = __floats2bfloat162_rn(c, d);
-    *reinterpret_cast<uint2 *>(p) =
-        make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
-}
-
-// Columns of a pair's tile (tcgen05 N: a multiple of 16), and of each quarter of the epilogue warps
-__device__ __forceinline__ int tile_columns(int rows) { return (rows + 15) & ~15; }
-__device__ __forceinline__ int quarter_columns(int cols) { return ((cols + 3) / 4 + 15) & ~15; }
-
-// ---- the epilogue --------------------------------------------------------------------
-// What one warp needs of its CTA: barrier arrays, the scales of this lane's columns, this
-// warp's tensor-memory lanes.
-struct Epilogue {
-    uint32_t acc_full, sc_full, sc_empty;
-    uint32_t acc_empty;  // the leader's (shared::cluster)
-    uint32_t tmem, scales;
-};
-
-// All blocks of a tile for 16 * STEPS columns from c0, then the stores.  The step
-// count is a template argument: with a branch per step the loads and FMAs of a
-// step cannot overlap (844 against 602 clocks a block, the loop alone).  False: a
-// wait ran out.
-template <int STEPS, class OUT, bool PERM>
-__device__ __forceinline__ bool epilogue_tile(const Epilogue &e, const ProductArgs &a, int c0, int rows, OUT *out,
-                                              int n_left, int &it)
-{
-    const int lane = threadIdx.x & 31;
-    float acc[2 * STEPS + 1][4][2];  // [column group][row group][column]
 #pragma unroll
-    for (int i = 0; i < 2 * STEPS; ++i)
+    for (int c = 0; c < kPart; c += 8) {
+        if (WIDE && c + 8 <= left) {
+            uint32_t w[8];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) acc[i][g][0] = acc[i][g][1] = 0.f;
-    for (int kb = 0; kb < a.kblocks; ++kb, ++it) {
-        const int d = it % kPairBufs, s = it % kPairScales;
-        const uint32_t pa = (it / kPairBufs) & 1, ps = (it / kPairScales) & 1;
-        const bool sc_ready = bar_try(e.sc_full + 8 * s, ps), acc_ready = bar_try(e.acc_full + 8 * d, pa);
-        if (!__all_sync(0xffffffffu, sc_ready && acc_ready)) {
-            const bool ok = bar_wait(e.sc_full + 8 * s, ps) && bar_wait(e.acc_full + 8 * d, pa);
-            if (!__all_sync(0xffffffffu, ok)) return false;
-        }
-        tc_fence_after_sync();
-        const uint32_t td = e.tmem + d * kPairTokens + c0;
-        const uint32_t sc = e.scales + (s * kScaleRow + c0 / 4) * 4;
+            for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(acc[c + j]);
+            store_sector(out + c, w);
+        } else {
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-            Frag f;
-            frag_request(td + 16 * i, f);
-            const float4 w4 = lds4(sc + 16 * i);
-            frag_wait();
-            if (i == STEPS - 1) {  // every value of the buffer has been read
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) pair_arrive(e.acc_empty + 8 * d);
-            }
-            const float w[2][2] = {{w4.x, w4.y}, {w4.z, w4.w}};
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    fma_volatile(acc[2 * i + q][0][b], f.v[4 * q + b], w[q][b]);
-                    fma_volatile(acc[2 * i + q][1][b], f.v[4 * q + 2 + b], w[q][b]);
-                    fma_volatile(acc[2 * i + q][2][b], f.w[4 * q + b], w[q][b]);
-                    fma_volatile(acc[2 * i + q][3][b], f.w[4 * q + 2 + b], w[q][b]);
-                }
-        }
-        __syncwarp();
-        if (lane == 0) {
-            if (STEPS == 0) pair_arrive(e.acc_empty + 8 * d);
-            bar_arrive(e.sc_empty + 8 * s);
+            for (int j = 0; j < 8; ++j)
+                if (c + j < left) out[c + j] = acc[c + j];
         }
     }
-    // out: column c0 + 2 (lane % 4), this lane's first weight row, of which n_left are left
-    const int64_t group = 8 * a.ld_out;
-    int left = rows - c0 - 2 * (lane & 3);
-    if (n_left <= 0) return true;
-#pragma unroll
-    for (int i = 0; i < 2 * STEPS; ++i, out += group, left -= 8) {
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            OUT *o = b ? out + a.ld_out : out;
-            if (left <= b) continue;
-            if (PERM) {
-                store4(o, acc[i][0][b], acc[i][1][b], acc[i][2][b], acc[i][3][b]);
-            } else {
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    if (8 * g < n_left) o[8 * g] = OUT(acc[i][g][b]);
-            }
-        }
-    }
-    return true;
 }
 
-// PERM: weight rows permuted by the tensor map (n a multiple of 32), 4-wide stores.
-template <class OUT, bool PERM>
+template <bool WIDE>
+__device__ __forceinline__ void store_row(__nv_bfloat16 *out, const float (&acc)[kPart], int left)
+{
+#pragma unroll
+    for (int c = 0; c < kPart; c += 16) {
+        if (WIDE && c + 16 <= left) {
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(acc[c + 2 * j], acc[c + 2 * j + 1]);
+                w[j] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+            store_sector(out + c, w);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (c + j < left) out[c + j] = __float2bfloat16_rn(acc[c + j]);
+        }
+    }
+}
+
+// The tile's token rows are split evenly between the CTAs; its columns (tcgen05 N) are a
+// multiple of 16.
+__device__ __forceinline__ int cta_rows(int rows) { return (rows + 1) / 2; }
+__device__ __forceinline__ int tile_columns(int left) { return left >= kPairWeights ? kPairWeights : (left + 15) & ~15; }
+
+// WIDE: output rows start on 32-byte boundaries.
+template <class OUT, bool WIDE>
 __global__ void __launch_bounds__(kPairThreads, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                     const ProductArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full[kPairStages], empty[kPairStages], acc_full[kPairBufs], acc_empty[kPairBufs],
-        sc_full[kPairScales], sc_empty[kPairScales], drain_bar;
+    __shared__ __align__(8) uint64_t full[kPairStages], empty[kPairStages], acc_full[kPairBufs], acc_empty[kPairBufs], drain_bar;
     __shared__ uint32_t tmem_base;
     __shared__ int warp_tiles[kPairThreads / 32];
     __shared__ volatile int abort_flag;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float *scale_ring = reinterpret_cast<float *>(smem + kPairStages * kPairStage);  // [slot][kScaleRow]
-    int *offset = reinterpret_cast<int *>(scale_ring + kPairScales * kScaleRow);
+    int *offset = reinterpret_cast<int *>(smem + kPairStages * kPairStage);
     int *first_tile = offset + kMaxExperts + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned rank = cluster_rank();
 
     if (warp == kMmaWarp) {
-        tmem_alloc2(&tmem_base, kPairBufs * kPairTokens);
+        tmem_alloc2(&tmem_base, kPairBufs * kPairWeights);
         tmem_relinquish2();
     }
     if (threadIdx.x == 0) {
@@ -346,10 +267,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             mbar_init(&acc_full[s], 1);
             mbar_init(&acc_empty[s], 2 * kEpiWarps);  // the epilogue warps of both CTAs (used by the leader)
         }
-        for (int s = 0; s < kPairScales; ++s) {
-            mbar_init(&sc_full[s], 2);
-            mbar_init(&sc_empty[s], kEpiWarps);
-        }
         mbar_init(&drain_bar, 1);
         abort_flag = 0;
         fence_mbar_init();
@@ -360,7 +277,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     cluster_sync();  // the other CTA's barriers and tensor memory exist from here on
     tc_fence_after_sync();
     const uint32_t tmem = tmem_base;
-    const int n_pairs = (a.n + 2 * kWeightRows - 1) / (2 * kWeightRows);
+    const int n_pairs = (a.n + kPairWeights - 1) / kPairWeights;
     const int n_work = first_tile[a.groups] * n_pairs;
     const int worker = blockIdx.x >> 1, workers = gridDim.x >> 1;
 
@@ -377,10 +294,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             bool go = true;
             for (int id = worker; id < n_work && go; id += workers) {
                 const Tile t = tile_at(id, n_pairs, a.groups, first_tile, offset);
-                const int mine = tile_columns(t.rows) / 2;  // token rows of each CTA
-                const int boxes = (mine + kBox - 1) / kBox;
+                const int mine = cta_rows(t.rows), boxes = (mine + kBox - 1) / kBox;
                 const uint32_t bytes = 2 * (kABytes + boxes * kBox * 128);
-                const int w0 = (t.n_tile * 2 + (int)rank) * kWeightRows, x0 = t.row0 + (int)rank * mine;
+                const int n0 = t.n_tile * kPairWeights, w0 = n0 + (int)rank * tile_columns(a.n - n0) / 2;
+                const int x0 = t.row0 + (int)rank * mine;
                 for (int kb = 0; kb < a.kblocks; ++kb, ++issued, r.next()) {
                     // the slot's previous use has been multiplied (a fresh slot passes)
                     if (!__all_sync(0xffffffffu, bar_wait(empty_at + 8 * r.slot, r.phase ^ 1))) {
@@ -388,11 +305,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         break;
                     }
                     if (elect_one()) {
-                        uint8_t *w_s = smem + r.slot * kPairStage, *x_s = w_s + kABytes;
+                        uint8_t *x_s = smem + r.slot * kPairStage, *w_s = x_s + kABytes;
                         if (rank == 0) mbar_arrive_expect_tx(&full[r.slot], bytes);
                         const uint32_t bar = leader_full + 8 * r.slot;
-                        if (PERM) tma2_load_5d(w_s, &map_w, bar, kb * 128, 0, 0, w0 / 32, t.group);
-                        else tma2_load_3d(w_s, &map_w, bar, kb * 128, w0, t.group);
+                        tma2_load_3d(w_s, &map_w, bar, kb * 128, w0, t.group);
                         for (int b = 0; b < boxes; ++b)
                             tma2_load_2d(x_s + b * kBox * 128, &map_x, bar, kb * 128, x0 + b * kBox);
                     }
@@ -409,13 +325,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             if (rank == 0) {
                 const uint32_t full_at = smem_u32(full), empty_at = smem_u32(empty), acc_full_at = smem_u32(acc_full),
                                acc_empty_at = smem_u32(acc_empty);
-                const uint64_t w_desc = desc_kmajor_sw128(smem), x_desc = desc_kmajor_sw128(smem + kABytes);
+                const uint64_t x_desc = desc_kmajor_sw128(smem), w_desc = desc_kmajor_sw128(smem + kABytes);
                 Ring<kPairStages> r;
                 Ring<kPairBufs> d;
                 bool go = true;
                 for (int id = worker; id < n_work && go; id += workers) {
                     const Tile t = tile_at(id, n_pairs, a.groups, first_tile, offset);
-                    const uint32_t idesc = idesc_e4m3(2 * kWeightRows, tile_columns(t.rows));
+                    const uint32_t idesc = idesc_e4m3(256, tile_columns(a.n - t.n_tile * kPairWeights));
                     for (int kb = 0; kb < a.kblocks; ++kb, r.next(), d.next()) {
                         const bool ok = bar_wait(full_at + 8 * r.slot, r.phase) &&
                                         bar_wait(acc_empty_at + 8 * d.slot, d.phase ^ 1);
@@ -429,7 +345,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                             const uint64_t wd = w_desc + step, xd = x_desc + step;
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                mma2_f8(tmem + d.slot * kPairTokens, wd + 2 * kk, xd + 2 * kk, idesc, kk != 0);
+                                mma2_f8(tmem + d.slot * kPairWeights, xd + 2 * kk, wd + 2 * kk, idesc, kk != 0);
                             mma2_commit(empty_at + 8 * r.slot);
                             mma2_commit(acc_full_at + 8 * d.slot);
                         }
@@ -442,76 +358,74 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     mbar_wait(&drain_bar, 0);
                 }
             }
-        } else {  // ---- scales of half of the columns
-            const int c0 = (warp - kScaleWarp0) * (kPairTokens / 2);
-            int it = 0;
-            bool go = true;
-            for (int id = worker; id < n_work && go; id += workers) {
-                const Tile t = tile_at(id, n_pairs, a.groups, first_tile, offset);
-                const int nb = t.n_tile * 2 + (int)rank;
-                const bool has_w = nb < a.n_tiles;
-                const float *bs = a.b_scale + ((int64_t)t.group * a.n_tiles + (has_w ? nb : 0)) * a.kblocks;
-                const float *as = a.a_scale + t.row0;
-                int at[4];  // this lane's columns, inside the tile
-#pragma unroll
-                for (int j = 0; j < 4; ++j) at[j] = min(c0 + j * 32 + lane, t.rows - 1);
-                for (int k0 = 0; k0 < a.kblocks && go; k0 += kScaleAhead) {
-                    // every load from a valid address, so that none waits behind a branch
-                    float v[kScaleAhead][4], w[kScaleAhead];
-#pragma unroll
-                    for (int i = 0; i < kScaleAhead; ++i) {
-                        const int kb = min(k0 + i, a.kblocks - 1);
-                        w[i] = __ldg(bs + kb);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) v[i][j] = __ldg(as + (int64_t)kb * a.ld_a_scale + at[j]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < kScaleAhead; ++i) {
-                        if (k0 + i >= a.kblocks) break;
-                        const int s = it % kPairScales, u = it / kPairScales;
-                        ++it;
-                        if (lane == 0) {
-                            go = u == 0 || mbar_wait(&sc_empty[s], (u - 1) & 1);
-                            if (!go) abort_flag = 1;
-                        }
-                        go = __shfl_sync(0xffffffffu, go, 0);
-                        if (!go) break;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int c = c0 + j * 32 + lane;
-                            scale_ring[s * kScaleRow + ((c & 7) >> 1) * kScaleStride + (c >> 3) * 2 + (c & 1)] = has_w ? v[i][j] * w[i] : 0.f;
-                        }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sc_full[s]);
-                    }
-                }
-            }
         }
     } else {  // ---- epilogue
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegs));
         const int part = warp >> 2, quarter = warp & 3;
-        const Epilogue e{smem_u32(acc_full),
-                         smem_u32(sc_full),
-                         smem_u32(sc_empty),
-                         cluster_map(smem_u32(acc_empty), 0),
-                         tmem + ((uint32_t)(quarter * 32) << 16),
-                         smem_u32(scale_ring + (lane & 3) * kScaleStride)};
-        int it = 0;
+        const uint32_t acc_full_at = smem_u32(acc_full), leader_empty = cluster_map(smem_u32(acc_empty), 0);
+        const uint32_t columns = tmem + ((uint32_t)(quarter * 32) << 16) + part * kPart;
+        Ring<kPairBufs> d;
         bool go = true;
         for (int id = worker; id < n_work && go; id += workers) {
             const Tile t = tile_at(id, n_pairs, a.groups, first_tile, offset);
-            const int all = tile_columns(t.rows), most = quarter_columns(all);
-            const int c0 = min(part * most, all), cols = min(most, all - c0);
-            const int n = (t.n_tile * 2 + (int)rank) * kWeightRows + quarter * 32 + (PERM ? 4 : 1) * (lane >> 2);
-            OUT *out = static_cast<OUT *>(a.out) + (int64_t)(t.row0 + c0 + 2 * (lane & 3)) * a.ld_out + n;
-            switch (cols / 16) {
-            case 0: go = epilogue_tile<0, OUT, PERM>(e, a, c0, t.rows, out, a.n - n, it); break;
-            case 1: go = epilogue_tile<1, OUT, PERM>(e, a, c0, t.rows, out, a.n - n, it); break;
-            case 2: go = epilogue_tile<2, OUT, PERM>(e, a, c0, t.rows, out, a.n - n, it); break;
-            case 3: go = epilogue_tile<3, OUT, PERM>(e, a, c0, t.rows, out, a.n - n, it); break;
-            default: go = epilogue_tile<4, OUT, PERM>(e, a, c0, t.rows, out, a.n - n, it); break;
+            const int mine = cta_rows(t.rows), n0 = t.n_tile * kPairWeights + part * kPart;
+            const int lane_row = quarter * 32 + lane, row = (int)rank * mine + lane_row;
+            const bool used = n0 < a.n && quarter * 32 < mine;  // this warp has outputs
+            const float *as = a.a_scale + t.row0 + min(row, t.rows - 1);
+            const float *bs = a.b_scale + ((int64_t)t.group * a.n_tiles + (used ? n0 / kWeightRows : 0)) * a.kblocks;
+            float acc[kPart];
+#pragma unroll
+            for (int c = 0; c < kPart; ++c) acc[c] = 0.f;
+            // one block: acc += scale * partial; false if the wait ran out
+            const auto block = [&](float scale) {
+                if (!__all_sync(0xffffffffu, bar_wait(acc_full_at + 8 * d.slot, d.phase))) return false;
+                tc_fence_after_sync();
+                if (used) {
+#pragma unroll
+                    for (int c = 0; c < kPart; c += kStep) {
+                        uint32_t v[kStep];
+                        columns_request(columns + d.slot * kPairWeights + c, v);
+                        columns_wait();
+                        if (c + kStep == kPart) {  // this warp has read its part of the buffer
+                            tc_fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) pair_arrive(leader_empty + 8 * d.slot);
+                        }
+#pragma unroll
+                        for (int j = 0; j < kStep; ++j) fma_volatile(acc[c + j], v[j], scale);
+                    }
+                } else if (lane == 0) {
+                    pair_arrive(leader_empty + 8 * d.slot);
+                }
+                d.next();
+                return true;
+            };
+            // two blocks a turn, with the next turn's scales loaded at its start
+            float s0 = __ldg(as) * __ldg(bs), s1 = 0.f;
+            if (a.kblocks > 1) s1 = __ldg(as + a.ld_a_scale) * __ldg(bs + 1);
+            for (int left = a.kblocks; left > 0 && go; left -= 2) {
+                float a2 = 0.f, b2 = 0.f, a3 = 0.f, b3 = 0.f;
+                as += 2 * a.ld_a_scale;
+                bs += 2;
+                if (left > 2) {
+                    a2 = load_ahead(as);
+                    b2 = load_ahead(bs);
+                }
+                if (left > 3) {
+                    a3 = load_ahead(as + a.ld_a_scale);
+                    b3 = load_ahead(bs + 1);
+                }
+                go = block(s0);
+                if (go && left > 1) go = block(s1);
+                s0 = a2 * b2;
+                s1 = a3 * b3;
             }
-            if (!go) abort_flag = 1;
+            if (!go) {
+                abort_flag = 1;
+                break;
+            }
+            if (used && lane_row < mine && row < t.rows)
+                store_row<WIDE>(static_cast<OUT *>(a.out) + (int64_t)(t.row0 + row) * a.ld_out + n0, acc, a.n - n0);
         }
     }
     __syncwarp();
@@ -520,28 +434,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     __syncthreads();
     cluster_sync();  // neither CTA leaves while the other may still arrive here or read its operands
     tc_fence_after_sync();
-    if (warp == kMmaWarp) tmem_dealloc2(tmem, kPairBufs * kPairTokens);
-}
-
-// Weight rows as [group][q][g][r][k] with row = 32 q + 4 r + g: a box of 128 rows puts
-// row 4 r + g of each 32 at shared-memory row 8 g + r.
-bool permuted_map(CUtensorMap *m, const Operands &o, const ProductArgs &a)
-{
-    const tmaps::EncodeTiledFn f = tmaps::encode_fn();
-    if (!f) return false;
-    cuuint64_t dims[5] = {(cuuint64_t)o.k, 8, 4, (cuuint64_t)(a.n / 32), (cuuint64_t)a.groups};
-    cuuint64_t strides[4] = {(cuuint64_t)o.ld_b * 4, (cuuint64_t)o.ld_b, (cuuint64_t)o.ld_b * 32, (cuuint64_t)o.stride_b};
-    cuuint32_t box[5] = {128, 8, 4, kWeightRows / 32, 1}, es[5] = {1, 1, 1, 1, 1};
-    return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<uint8_t *>(o.b), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    if (warp == kMmaWarp) tmem_dealloc2(tmem, kPairBufs * kPairWeights);
 }
 
 template <class OUT>
-cudaError_t pair_launch(const CUtensorMap &mw, const CUtensorMap &mx, const ProductArgs &a, bool perm, int pairs,
+cudaError_t pair_launch(const CUtensorMap &mw, const CUtensorMap &mx, const ProductArgs &a, bool wide, int pairs,
                         cudaStream_t s)
 {
-    return perm ? launch(fp8_pair_kernel<OUT, true>, dim3(2 * pairs), kPairThreads, kPairSmem, s, 2, false, mw, mx, a)
+    return wide ? launch(fp8_pair_kernel<OUT, true>, dim3(2 * pairs), kPairThreads, kPairSmem, s, 2, false, mw, mx, a)
                 : launch(fp8_pair_kernel<OUT, false>, dim3(2 * pairs), kPairThreads, kPairSmem, s, 2, false, mw, mx, a);
 }
 
@@ -560,13 +460,13 @@ cudaError_t pair_prepare()
 moe_status pair_product(const Operands &o, const ProductArgs &a, moe_dtype out_dtype, int pairs, cudaStream_t s)
 {
     const bool bf16 = out_dtype == MOE_DT_BF16;
-    const bool perm = a.n % 32 == 0 && a.ld_out % 4 == 0 && aligned(a.out, bf16 ? 8 : 16);
+    // 32-byte stores where every output row starts on a sector
+    const bool wide = aligned(a.out, 32) && a.ld_out * (bf16 ? 2 : 4) % 32 == 0;
     CUtensorMap mw, mx;
-    if (perm ? !permuted_map(&mw, o, a) : !code_map(&mw, o.b, o.k, a.n, o.ld_b, a.groups, o.stride_b, kWeightRows))
-        return MOE_ERR_CUDA;
+    if (!code_map(&mw, o.b, o.k, a.n, o.ld_b, a.groups, o.stride_b, kPairWeights / 2)) return MOE_ERR_CUDA;
     if (!code_map(&mx, o.a, o.k, a.rows, o.ld_a, 0, 0, kBox)) return MOE_ERR_CUDA;
-    return launched(bf16 ? pair_launch<__nv_bfloat16>(mw, mx, a, perm, pairs, s)
-                         : pair_launch<float>(mw, mx, a, perm, pairs, s));
+    return launched(bf16 ? pair_launch<__nv_bfloat16>(mw, mx, a, wide, pairs, s)
+                         : pair_launch<float>(mw, mx, a, wide, pairs, s));
 }
 
 }  // namespace fp8
