@@ -12,17 +12,17 @@
 // the epilogue, which skip.
 //
 // The epilogue is the other bound: 128 x 256 fused multiply-adds a block and CTA,
-// 256 clocks of the FMA pipes.  Tokens on the lanes give a thread one row: its scale is
-// one register, loaded two blocks ahead, and one product with the weights' block
-// scale covers all its columns.  (With the weights on the lanes, as in the kernel
-// for few rows, every column has a scale of its own, read from shared memory:
-// 153.7 us at 8192 x 4096 x 4096.)  Sixteen warps, four per scheduler, hide the barrier
-// and tensor-memory latencies of one another.
+// 256 clocks of the FMA pipes, and a chain of latencies (MMA, commit, wait, read, release)
+// over the two buffers: 784 clocks a block measured.  Tokens on the lanes give a thread
+// one row: its scale is one register, loaded two blocks ahead, and one product with the
+// weights' block scale covers all its columns.  (With the weights on the lanes, as in
+// the kernel for few rows, every column has a scale of its own, read from shared memory:
+// 153.7 us at 8192 x 4096 x 4096.)
 //
-//   warps 0-15   epilogue: warpgroup q owns columns 64 q .. 64 q + 63
-//   warp 16      TMA producer (both CTAs; all bytes count on the leader's barrier)
-//   warp 17      MMA issuer (the leader's only)
-//   warps 18-19  idle (a register split works on groups of four warps)
+//   warps 0-7    epilogue: warpgroup h owns columns 128 h .. 128 h + 127
+//   warp 8       TMA producer (both CTAs; all bytes count on the leader's barrier)
+//   warp 9       MMA issuer (the leader's only)
+//   warps 10-11  idle (a register split works on groups of four warps)
 // Every mbarrier wait is bounded.
 #include "fp8_common.cuh"
 
@@ -30,18 +30,21 @@ namespace moe {
 namespace fp8 {
 namespace {
 
-constexpr int kEpiWarps = 16;
+constexpr int kEpiWarps = 8;
 constexpr int kTmaWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
 constexpr int kPairThreads = 32 * (kEpiWarps + 4);
-constexpr int kPairStages = 6, kPairBufs = 2;
+constexpr int kPairStages = 4, kPairBufs = 2;
 constexpr int kPairWeights = 256;          // weight rows (accumulator columns) of a tile
-constexpr int kPart = kPairWeights / 4;    // columns of a warpgroup
+constexpr int kPart = kPairWeights * 4 / kEpiWarps;    // columns of a warpgroup
 constexpr int kBox = 32;                   // token rows of one TMA box
 constexpr int kPairStage = 2 * kABytes;    // 128 token rows, 128 weight rows
-constexpr int kPairSmem = kPairStages * kPairStage + 2 * (kMaxExperts + 1) * 4 + 1024;
-// registers: 640 threads at 96 are 512 at 112 and 128 at 32
-constexpr int kEpilogueRegs = 112, kOtherRegs = 32;
-static_assert(32 * kEpiWarps * kEpilogueRegs + 128 * kOtherRegs <= kPairThreads * 96, "register split exceeds the launch's");
+constexpr int kBoxBytes = 32 * 128;        // an output box: 32 rows of 128 bytes
+constexpr int kOutBytes = 2 * kBoxBytes;   // a warp's output stage
+constexpr int kPairSmem =
+    kPairStages * kPairStage + kEpiWarps * kOutBytes + 2 * (kMaxExperts + 1) * 4 + 1024;
+// registers: 384 threads at 168 are 256 at 216 and 128 at 72
+constexpr int kEpilogueRegs = 216, kOtherRegs = 72;
+static_assert(32 * kEpiWarps * kEpilogueRegs + 128 * kOtherRegs <= kPairThreads * 168, "register split exceeds the launch's");
 
 // ---- shared memory by 32-bit addresses --------------------------------------------------
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
@@ -154,16 +157,18 @@ __device__ __forceinline__ void pair_arrive(uint32_t bar)
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// 16 columns of this thread's lane; valid after columns_wait.  They are no operands of the
+// 32 columns of this thread's lane; valid after columns_wait.  They are no operands of the
 // wait (they would be copied); the FMAs that use them are volatile and stay behind it.
-// (32 at a time leave too few registers: spilled loop variables cost 1000 clocks a turn.)
-constexpr int kStep = 16;
+constexpr int kStep = 32;
 __device__ __forceinline__ void columns_request(uint32_t taddr, uint32_t (&v)[kStep])
 {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(taddr));
 }
 
@@ -184,50 +189,79 @@ __device__ __forceinline__ void fma_volatile(float &acc, uint32_t v, float s)
     asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(__uint_as_float(v)), "f"(s));
 }
 
-// 32 bytes (a whole sector) of one output row
-__device__ __forceinline__ void store_sector(void *p, const uint32_t (&w)[8])
+// ---- stores -----------------------------------------------------------------------------
+// A warp's 32 rows go through shared memory (128-byte rows in the 128-byte swizzle) and
+// leave as TMA boxes: a thread's own row would be 32 lines an instruction, and the epilogue
+// would wait for them before the next tile (131.3 us at 8192 x 4096 x 4096).
+__device__ __forceinline__ void tma_store_2d(const void *tmap, uint32_t src, int c0, int c1)
 {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(tmap), "r"(src),
+                 "r"(c0), "r"(c1)
                  : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-// `left` columns (of 64) of one row; WIDE: the row starts on 32 bytes.
-template <bool WIDE>
-__device__ __forceinline__ void store_row(float *out, const float (&acc)[kPart], int left)
+// this thread's stores have left shared memory / have been written
+__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ uint4 pack16(const float *v, float)
 {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+
+__device__ __forceinline__ uint4 pack16(const float *v, __nv_bfloat16)
+{
+    uint32_t w[4];
 #pragma unroll
-    for (int c = 0; c < kPart; c += 8) {
-        if (WIDE && c + 8 <= left) {
-            uint32_t w[8];
+    for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The warp's columns of its 32 rows, all of them inside the tile, two boxes at a time.
+template <class OUT>
+__device__ __forceinline__ void store_rows(const CUtensorMap *map, uint32_t stage, const float (&acc)[kPart], int row0,
+                                           int n0, int n)
+{
+    constexpr int per = 16 / sizeof(OUT), cols = 128 / sizeof(OUT);  // columns of 16 bytes, of a box
+    int lane;  // volatile: addresses computed from it are not kept in registers over the block loop
+    asm volatile("mov.u32 %0, %%laneid;" : "=r"(lane));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(acc[c + j]);
-            store_sector(out + c, w);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c + j < left) out[c + j] = acc[c + j];
+    for (int c = 0; c < kPart; c += cols) {
+        const uint32_t box = stage + (c / cols & 1) * kBoxBytes;
+        if ((c / cols & 1) == 0) {
+            if (lane == 0) stores_read();
+            __syncwarp();
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint4 w = pack16(acc + c + j * per, OUT());
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * 128 + ((j ^ (lane & 7)) << 4)),
+                         "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
+                         : "memory");
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && n0 + c < n) tma_store_2d(map, box, n0 + c, row0);
     }
 }
 
-template <bool WIDE>
-__device__ __forceinline__ void store_row(__nv_bfloat16 *out, const float (&acc)[kPart], int left)
+// `left` columns (of the warp's part) of one row; WIDE: the row starts on 16 bytes.
+template <bool WIDE, class OUT>
+__device__ __forceinline__ void store_row(OUT *out, const float (&acc)[kPart], int left)
 {
+    constexpr int per = 16 / sizeof(OUT);
 #pragma unroll
-    for (int c = 0; c < kPart; c += 16) {
-        if (WIDE && c + 16 <= left) {
-            uint32_t w[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(acc[c + 2 * j], acc[c + 2 * j + 1]);
-                w[j] = *reinterpret_cast<const uint32_t *>(&b);
-            }
-            store_sector(out + c, w);
+    for (int c = 0; c < kPart; c += per) {
+        if (WIDE && c + per <= left) {
+            *reinterpret_cast<uint4 *>(out + c) = pack16(acc + c, OUT());
         } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (c + j < left) out[c + j] = __float2bfloat16_rn(acc[c + j]);
+            for (int j = 0; j < per; ++j)
+                if (c + j < left) out[c + j] = OUT(acc[c + j]);
         }
     }
 }
@@ -237,11 +271,56 @@ __device__ __forceinline__ void store_row(__nv_bfloat16 *out, const float (&acc)
 __device__ __forceinline__ int cta_rows(int rows) { return (rows + 1) / 2; }
 __device__ __forceinline__ int tile_columns(int left) { return left >= kPairWeights ? kPairWeights : (left + 15) & ~15; }
 
-// WIDE: output rows start on 32-byte boundaries.
+// A warp's walk over its tiles (id, id + workers, ...): weight tile and token tile advance without
+// a division, the group by a search of 32 at a time from the last one.
+struct TileWalk {
+    int token_tile, n_tile, group, step_token, step_n, n_tiles;
+    __device__ __forceinline__ TileWalk(int id, int workers, int n_tiles_)
+        : token_tile(id / n_tiles_), n_tile(id % n_tiles_), group(0), step_token(workers / n_tiles_),
+          step_n(workers % n_tiles_), n_tiles(n_tiles_)
+    {
+    }
+    __device__ __forceinline__ void next()
+    {
+        token_tile += step_token;
+        n_tile += step_n;
+        if (n_tile >= n_tiles) {
+            n_tile -= n_tiles;
+            ++token_tile;
+        }
+    }
+    // the whole warp, converged
+    __device__ __forceinline__ Tile tile(int groups, const int *first_tile, const int *offset)
+    {
+        const int lane = threadIdx.x & 31;
+        for (;;) {  // groups whose successor starts at or before this token tile
+            const int g = group + lane;
+            const unsigned passed = __ballot_sync(0xffffffffu, g < groups - 1 && first_tile[min(g, groups - 1) + 1] <= token_tile);
+            group += __popc(passed);
+            if (passed != 0xffffffffu) break;
+        }
+        Tile t;
+        t.group = group;
+        t.n_tile = n_tile;
+        const int first = first_tile[group], parts = first_tile[group + 1] - first;
+        const int lo = offset[group], rows = offset[group + 1] - lo;
+        if (parts == 1) {
+            t.row0 = lo;
+            t.rows = rows;
+        } else {
+            const int size = (((rows + parts - 1) / parts) + 15) & ~15;
+            t.row0 = lo + (token_tile - first) * size;
+            t.rows = min(size, lo + rows - t.row0);
+        }
+        return t;
+    }
+};
+
+// WIDE: output rows start on 16-byte boundaries (map_y is then a map of the output).
 template <class OUT, bool WIDE>
 __global__ void __launch_bounds__(kPairThreads, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
-                    const ProductArgs a)
+                    const __grid_constant__ CUtensorMap map_y, const ProductArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[kPairStages], empty[kPairStages], acc_full[kPairBufs], acc_empty[kPairBufs], drain_bar;
@@ -249,7 +328,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     __shared__ int warp_tiles[kPairThreads / 32];
     __shared__ volatile int abort_flag;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    int *offset = reinterpret_cast<int *>(smem + kPairStages * kPairStage);
+    uint8_t *out_stage = smem + kPairStages * kPairStage;  // [warp][32][128]
+    int *offset = reinterpret_cast<int *>(out_stage + kEpiWarps * kOutBytes);
     int *first_tile = offset + kMaxExperts + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned rank = cluster_rank();
@@ -292,8 +372,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             Ring<kPairStages> r;
             int issued = 0;
             bool go = true;
-            for (int id = worker; id < n_work && go; id += workers) {
-                const Tile t = tile_at(id, n_pairs, a.groups, first_tile, offset);
+            TileWalk walk(worker, workers, n_pairs);
+            for (int id = worker; id < n_work && go; id += workers, walk.next()) {
+                const Tile t = walk.tile(a.groups, first_tile, offset);
                 const int mine = cta_rows(t.rows), boxes = (mine + kBox - 1) / kBox;
                 const uint32_t bytes = 2 * (kABytes + boxes * kBox * 128);
                 const int n0 = t.n_tile * kPairWeights, w0 = n0 + (int)rank * tile_columns(a.n - n0) / 2;
@@ -329,9 +410,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 Ring<kPairStages> r;
                 Ring<kPairBufs> d;
                 bool go = true;
-                for (int id = worker; id < n_work && go; id += workers) {
-                    const Tile t = tile_at(id, n_pairs, a.groups, first_tile, offset);
-                    const uint32_t idesc = idesc_e4m3(256, tile_columns(a.n - t.n_tile * kPairWeights));
+                TileWalk walk(worker, workers, n_pairs);
+                for (int id = worker; id < n_work && go; id += workers, walk.next()) {
+                    const uint32_t idesc = idesc_e4m3(256, tile_columns(a.n - walk.n_tile * kPairWeights));
                     for (int kb = 0; kb < a.kblocks; ++kb, r.next(), d.next()) {
                         const bool ok = bar_wait(full_at + 8 * r.slot, r.phase) &&
                                         bar_wait(acc_empty_at + 8 * d.slot, d.phase ^ 1);
@@ -364,69 +445,77 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const int part = warp >> 2, quarter = warp & 3;
         const uint32_t acc_full_at = smem_u32(acc_full), leader_empty = cluster_map(smem_u32(acc_empty), 0);
         const uint32_t columns = tmem + ((uint32_t)(quarter * 32) << 16) + part * kPart;
-        Ring<kPairBufs> d;
+        int it = 0;  // block of the CTA: buffer it % 2
         bool go = true;
-        for (int id = worker; id < n_work && go; id += workers) {
-            const Tile t = tile_at(id, n_pairs, a.groups, first_tile, offset);
+        TileWalk walk(worker, workers, n_pairs);
+        for (int id = worker; id < n_work; id += workers, walk.next()) {
+            const Tile t = walk.tile(a.groups, first_tile, offset);
             const int mine = cta_rows(t.rows), n0 = t.n_tile * kPairWeights + part * kPart;
-            const int lane_row = quarter * 32 + lane, row = (int)rank * mine + lane_row;
-            const bool used = n0 < a.n && quarter * 32 < mine;  // this warp has outputs
-            const float *as = a.a_scale + t.row0 + min(row, t.rows - 1);
-            const float *bs = a.b_scale + ((int64_t)t.group * a.n_tiles + (used ? n0 / kWeightRows : 0)) * a.kblocks;
+            const int row0 = t.row0 + (int)rank * mine + quarter * 32;
+            // rows of this warp that have outputs
+            const int rows = n0 < a.n ? min(mine, t.rows - (int)rank * mine) - quarter * 32 : 0;
+            const float *as = a.a_scale + min(row0 + lane, t.row0 + t.rows - 1);
+            const float *bs = a.b_scale + ((int64_t)t.group * a.n_tiles + min(n0, a.n - 1) / kWeightRows) * a.kblocks;
+            float a0 = load_ahead(as), b0 = load_ahead(bs), a1 = 0.f, b1 = 0.f;
+            if (a.kblocks > 1) {
+                a1 = load_ahead(as + a.ld_a_scale);
+                b1 = load_ahead(bs + 1);
+            }
             float acc[kPart];
 #pragma unroll
             for (int c = 0; c < kPart; ++c) acc[c] = 0.f;
             // one block: acc += scale * partial; false if the wait ran out
             const auto block = [&](float scale) {
-                if (!__all_sync(0xffffffffu, bar_wait(acc_full_at + 8 * d.slot, d.phase))) return false;
+                const uint32_t d = it & 1;
+                if (!__all_sync(0xffffffffu, bar_wait(acc_full_at + 8 * d, (it >> 1) & 1))) return false;
+                ++it;
                 tc_fence_after_sync();
-                if (used) {
+                if (rows > 0) {
 #pragma unroll
                     for (int c = 0; c < kPart; c += kStep) {
                         uint32_t v[kStep];
-                        columns_request(columns + d.slot * kPairWeights + c, v);
+                        columns_request(columns + d * kPairWeights + c, v);
                         columns_wait();
                         if (c + kStep == kPart) {  // this warp has read its part of the buffer
                             tc_fence_before_sync();
                             __syncwarp();
-                            if (lane == 0) pair_arrive(leader_empty + 8 * d.slot);
+                            if (lane == 0) pair_arrive(leader_empty + 8 * d);
                         }
 #pragma unroll
                         for (int j = 0; j < kStep; ++j) fma_volatile(acc[c + j], v[j], scale);
                     }
                 } else if (lane == 0) {
-                    pair_arrive(leader_empty + 8 * d.slot);
+                    pair_arrive(leader_empty + 8 * d);
                 }
-                d.next();
                 return true;
             };
             // two blocks a turn, with the next turn's scales loaded at its start
-            float s0 = __ldg(as) * __ldg(bs), s1 = 0.f;
-            if (a.kblocks > 1) s1 = __ldg(as + a.ld_a_scale) * __ldg(bs + 1);
             for (int left = a.kblocks; left > 0 && go; left -= 2) {
-                float a2 = 0.f, b2 = 0.f, a3 = 0.f, b3 = 0.f;
+                const float s0 = a0 * b0;
                 as += 2 * a.ld_a_scale;
                 bs += 2;
                 if (left > 2) {
-                    a2 = load_ahead(as);
-                    b2 = load_ahead(bs);
-                }
-                if (left > 3) {
-                    a3 = load_ahead(as + a.ld_a_scale);
-                    b3 = load_ahead(bs + 1);
+                    a0 = load_ahead(as);
+                    b0 = load_ahead(bs);
                 }
                 go = block(s0);
+                const float s1 = a1 * b1;
+                if (left > 3) {
+                    a1 = load_ahead(as + a.ld_a_scale);
+                    b1 = load_ahead(bs + 1);
+                }
                 if (go && left > 1) go = block(s1);
-                s0 = a2 * b2;
-                s1 = a3 * b3;
             }
             if (!go) {
                 abort_flag = 1;
                 break;
             }
-            if (used && lane_row < mine && row < t.rows)
-                store_row<WIDE>(static_cast<OUT *>(a.out) + (int64_t)(t.row0 + row) * a.ld_out + n0, acc, a.n - n0);
+            if (WIDE && rows >= 32)
+                store_rows<OUT>(&map_y, smem_u32(out_stage) + warp * kOutBytes, acc, row0, n0, a.n);
+            else if (lane < rows)
+                store_row<WIDE>(static_cast<OUT *>(a.out) + (int64_t)(row0 + lane) * a.ld_out + n0, acc, a.n - n0);
         }
+        if (WIDE && lane == 0) stores_done();
     }
     __syncwarp();
     if (abort_flag && threadIdx.x == 0 && a.status) atomicExch(a.status, (int)MOE_ERR_TIMEOUT);
@@ -437,12 +526,26 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (warp == kMmaWarp) tmem_dealloc2(tmem, kPairBufs * kPairWeights);
 }
 
-template <class OUT>
-cudaError_t pair_launch(const CUtensorMap &mw, const CUtensorMap &mx, const ProductArgs &a, bool wide, int pairs,
-                        cudaStream_t s)
+// The output as boxes of 32 rows x 128 bytes.
+bool out_map(CUtensorMap *m, const ProductArgs &a, bool bf16)
 {
-    return wide ? launch(fp8_pair_kernel<OUT, true>, dim3(2 * pairs), kPairThreads, kPairSmem, s, 2, false, mw, mx, a)
-                : launch(fp8_pair_kernel<OUT, false>, dim3(2 * pairs), kPairThreads, kPairSmem, s, 2, false, mw, mx, a);
+    const tmaps::EncodeTiledFn f = tmaps::encode_fn();
+    if (!f) return false;
+    const int size = bf16 ? 2 : 4;
+    cuuint64_t dims[2] = {(cuuint64_t)a.n, (cuuint64_t)a.rows};
+    cuuint64_t strides[1] = {(cuuint64_t)a.ld_out * size};
+    cuuint32_t box[2] = {(cuuint32_t)(128 / size), 32}, es[2] = {1, 1};
+    return f(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, a.out, dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class OUT>
+cudaError_t pair_launch(const CUtensorMap &mw, const CUtensorMap &mx, const CUtensorMap &my, const ProductArgs &a,
+                        bool wide, int pairs, cudaStream_t s)
+{
+    return wide ? launch(fp8_pair_kernel<OUT, true>, dim3(2 * pairs), kPairThreads, kPairSmem, s, 2, false, mw, mx, my, a)
+                : launch(fp8_pair_kernel<OUT, false>, dim3(2 * pairs), kPairThreads, kPairSmem, s, 2, false, mw, mx, my, a);
 }
 
 }  // namespace
@@ -460,13 +563,13 @@ cudaError_t pair_prepare()
 moe_status pair_product(const Operands &o, const ProductArgs &a, moe_dtype out_dtype, int pairs, cudaStream_t s)
 {
     const bool bf16 = out_dtype == MOE_DT_BF16;
-    // 32-byte stores where every output row starts on a sector
-    const bool wide = aligned(a.out, 32) && a.ld_out * (bf16 ? 2 : 4) % 32 == 0;
-    CUtensorMap mw, mx;
+    const bool wide = aligned(a.out, 16) && a.ld_out * (bf16 ? 2 : 4) % 16 == 0 && a.ld_out < 1ll << 37;
+    CUtensorMap mw, mx, my{};
     if (!code_map(&mw, o.b, o.k, a.n, o.ld_b, a.groups, o.stride_b, kPairWeights / 2)) return MOE_ERR_CUDA;
     if (!code_map(&mx, o.a, o.k, a.rows, o.ld_a, 0, 0, kBox)) return MOE_ERR_CUDA;
-    return launched(bf16 ? pair_launch<__nv_bfloat16>(mw, mx, a, wide, pairs, s)
-                         : pair_launch<float>(mw, mx, a, wide, pairs, s));
+    if (wide && !out_map(&my, a, bf16)) return MOE_ERR_CUDA;
+    return launched(bf16 ? pair_launch<__nv_bfloat16>(mw, mx, my, a, wide, pairs, s)
+                         : pair_launch<float>(mw, mx, my, a, wide, pairs, s));
 }
 
 }  // namespace fp8
