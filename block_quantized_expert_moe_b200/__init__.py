@@ -416,244 +416,6 @@ def moe_get_device_error(pack):
     return lib.moe_get_device_error(pack.handle)
 
 
-# ---- operators beside the layer ------------------------------------------------------
-# Each runs on its tensors' device, on `stream` or that device's current stream.
-
-def _float_code(t, name):
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor, not {type(t).__name__}")
-    if t.dtype == torch.bfloat16:
-        return MOE_DT_BF16
-    if t.dtype == torch.float32:
-        return MOE_DT_F32
-    raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, not {t.dtype}")
-
-
-def _rows_of(t, name, dtypes, shape):
-    """A tensor whose last dimension is contiguous and whose rows do not overlap; returns the row stride."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor, not {type(t).__name__}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    cols = shape[-1]
-    if cols > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-    if shape[-2] > 1:
-        ld = t.stride(-2)
-        if ld < cols:
-            raise ValueError(f"{name}'s rows must not overlap")
-        return ld
-    return cols  # one row (or none): its stride is never used
-
-
-def _code_rows(t, name, shape):
-    """Rows of E4M3 codes: their stride in bytes, a multiple of 16."""
-    import torch
-    ld = _rows_of(t, name, (torch.float8_e4m3fn, torch.uint8), shape)
-    if shape[-2] <= 1:
-        return -(-ld // 16) * 16
-    if ld % 16:
-        raise ValueError(f"{name}'s rows must start on multiples of 16 bytes (row stride {ld}): "
-                         "allocate them a multiple of 16 wide and take the first columns")
-    return ld
-
-
-def _run(fn, what, named, args, stream):
-    """Checks that every tensor is on one CUDA device, then calls fn(*args, stream) with that device current."""
-    import torch
-    device = None
-    for name, t in named:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor: the library reads and writes device memory")
-        if device is None:
-            device = t.device.index
-        elif t.device.index != device:
-            raise ValueError(f"{name} is on cuda:{t.device.index}, expected cuda:{device}")
-    if torch.cuda.current_device() != device:
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream_ptr(stream)), what)
-    else:
-        _check(fn(*args, _stream_ptr(stream)), what)
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def moe_expert_plan(idx, n_experts, counts, offsets, rows, slots, stream=None):
-    """The (token, choice) pairs of idx (CUDA int32 [T, k], as moe_route_topk writes
-    it; values outside [0, n_experts) are no choice) sorted by expert: counts
-    int32 [E], offsets int32 [E + 1], rows int32 [T * k] (each slot's token, -1
-    behind the last one in use), slots int32 [T, k] (each pair's slot or -1)."""
-    import torch
-    T, k = _shape2(idx, "idx")
-    i32 = (torch.int32,)
-    _check_tensor(idx, "idx", i32, (T, k))
-    _check_tensor(counts, "counts", i32, (n_experts,))
-    _check_tensor(offsets, "offsets", i32, (n_experts + 1,))
-    _check_tensor(rows, "rows", i32, (T * k,))
-    _check_tensor(slots, "slots", i32, (T, k))
-    _run(lib.moe_expert_plan, "moe_expert_plan",
-         (("idx", idx), ("counts", counts), ("offsets", offsets), ("rows", rows), ("slots", slots)),
-         (idx.data_ptr(), T, k, n_experts, counts.data_ptr(), offsets.data_ptr(), rows.data_ptr(), slots.data_ptr()),
-         stream)
-
-
-def moe_balance_loss_workspace_bytes(n_tokens, n_experts):
-    return lib.moe_balance_loss_workspace_bytes(n_tokens, n_experts)
-
-
-def _check_valid(valid, T):
-    import torch
-    if valid is not None:
-        _check_tensor(valid, "valid", (torch.bool, torch.uint8), (T,))
-
-
-def moe_balance_loss(logits, idx, counts, prob_mean, loss, workspace=None, valid=None, stream=None):
-    """Balance loss of router logits (CUDA [T, E] float32/bfloat16) and choices idx
-    (int32 [T, k]) over the tokens `valid` marks (bool/uint8 [T]; None: all):
-    loss float32 [1] = sum_e f_e P_e, counts int32 [E + 1] (choices per expert, then
-    the tokens that count), prob_mean float32 [E] (P).  workspace: CUDA tensor of
-    moe_balance_loss_workspace_bytes(T, E) bytes (None when that is 0)."""
-    import torch
-    T, E = _shape2(logits, "logits")
-    k = _shape2(idx, "idx")[1]
-    dt = _float_code(logits, "logits")
-    _check_tensor(logits, "logits", (logits.dtype,), (T, E))
-    _check_tensor(idx, "idx", (torch.int32,), (T, k))
-    _check_tensor(counts, "counts", (torch.int32,), (E + 1,))
-    _check_tensor(prob_mean, "prob_mean", (torch.float32,), (E,))
-    _check_tensor(loss, "loss", (torch.float32,), (1,))
-    _check_valid(valid, T)
-    ws_bytes = 0
-    if workspace is not None:
-        _check_tensor(workspace, "workspace", (workspace.dtype,), workspace.shape)
-        ws_bytes = workspace.numel() * workspace.element_size()
-    _run(lib.moe_balance_loss, "moe_balance_loss",
-         (("logits", logits), ("idx", idx), ("valid", valid), ("counts", counts), ("prob_mean", prob_mean),
-          ("loss", loss), ("workspace", workspace)),
-         (logits.data_ptr(), dt, idx.data_ptr(), _ptr(valid), T, E, k, loss.data_ptr(), counts.data_ptr(),
-          prob_mean.data_ptr(), _ptr(workspace), ws_bytes), stream)
-
-
-def moe_balance_loss_backward(logits, counts, top_k, dloss, dlogits, valid=None, stream=None):
-    """Gradient of moe_balance_loss: dlogits (type and shape of logits) from the counts
-    it wrote and dloss (float32 [1], the gradient of the loss)."""
-    import torch
-    T, E = _shape2(logits, "logits")
-    dt = _float_code(logits, "logits")
-    _check_tensor(logits, "logits", (logits.dtype,), (T, E))
-    _check_tensor(counts, "counts", (torch.int32,), (E + 1,))
-    _check_tensor(dloss, "dloss", (torch.float32,), (1,))
-    _check_tensor(dlogits, "dlogits", (logits.dtype,), (T, E))
-    _check_valid(valid, T)
-    _run(lib.moe_balance_loss_backward, "moe_balance_loss_backward",
-         (("logits", logits), ("counts", counts), ("valid", valid), ("dloss", dloss), ("dlogits", dlogits)),
-         (logits.data_ptr(), dt, counts.data_ptr(), _ptr(valid), dloss.data_ptr(), T, E, top_k, dlogits.data_ptr()),
-         stream)
-
-
-def moe_fp8_quantize(x, codes, scales, rows=None, swiglu=False, stream=None):
-    """E4M3 codes [R, C] (float8_e4m3fn or uint8, rows on multiples of 16 bytes) and
-    float32 scales [ceil(C / 128), R] of x (CUDA float32/bfloat16): of its rows [R, C],
-    of rows[r] for output row r (rows int32 [R]; an index outside x gives zeros),
-    or, with swiglu, of silu(x[:, :C]) * x[:, C:] for x [R, 2 C]."""
-    import torch
-    S, W = _shape2(x, "x")
-    R, C = _shape2(codes, "codes")
-    dt = _float_code(x, "x")
-    if W != (2 * C if swiglu else C):
-        raise ValueError(f"x must have {2 * C if swiglu else C} columns, not {W}")
-    if rows is None:
-        if S != R:
-            raise ValueError(f"x must have {R} rows, not {S}")
-    else:
-        _check_tensor(rows, "rows", (torch.int32,), (R,))
-    ld_x = _rows_of(x, "x", (x.dtype,), (S, W))
-    ld_c = _code_rows(codes, "codes", (R, C))
-    ld_s = _rows_of(scales, "scales", (torch.float32,), (-(-C // 128), R))
-    _run(lib.moe_fp8_quantize, "moe_fp8_quantize", (("x", x), ("rows", rows), ("codes", codes), ("scales", scales)),
-         (x.data_ptr(), dt, ld_x, _ptr(rows), S, R, C, 1 if swiglu else 0, codes.data_ptr(), ld_c, scales.data_ptr(),
-          ld_s), stream)
-
-
-def _matrices(t, name):
-    if len(getattr(t, "shape", ())) not in (2, 3):
-        raise ValueError(f"{name} must be 2-D or 3-D, not of shape {tuple(getattr(t, 'shape', ()))}")
-    return tuple(t.shape) if t.dim() == 3 else (1,) + tuple(t.shape)
-
-
-def moe_fp8_quantize_weight(w, codes, scales, stream=None):
-    """E4M3 codes of w (CUDA float32/bfloat16 [N, K] or [G, N, K]) with a float32 scale
-    per 128 x 128 block: scales [ceil(N / 128), ceil(K / 128)] or [G, ...]."""
-    import torch
-    G, N, K = _matrices(w, "w")
-    dt = _float_code(w, "w")
-    ld_w = _rows_of(w, "w", (w.dtype,), w.shape)
-    ld_c = _code_rows(codes, "codes", w.shape)
-    _check_tensor(scales, "scales", (torch.float32,), tuple(w.shape[:-2]) + (-(-N // 128), -(-K // 128)))
-    gs_w, gs_c = (w.stride(0), codes.stride(0)) if G > 1 else (0, 0)
-    _run(lib.moe_fp8_quantize_weight, "moe_fp8_quantize_weight", (("w", w), ("codes", codes), ("scales", scales)),
-         (w.data_ptr(), dt, ld_w, gs_w, G, N, K, codes.data_ptr(), ld_c, gs_c, scales.data_ptr()), stream)
-
-
-def _check_status(status):
-    import torch
-    if status is not None:
-        _check_tensor(status, "status", (torch.int32,), (1,))
-
-
-def moe_fp8_matmul(a, a_scale, b, b_scale, out, status=None, stream=None):
-    """out [R, N] (CUDA float32/bfloat16) = (a with a_scale) (b with b_scale)^T: a [R, K]
-    and b [N, K] E4M3 codes (float8_e4m3fn or uint8, rows on multiples of 16 bytes),
-    a_scale float32 [ceil(K / 128), R], b_scale float32 [ceil(N / 128), ceil(K / 128)].
-    status: int32 [1] that takes MOE_ERR_TIMEOUT if a device-side wait runs out."""
-    import torch
-    R, K = _shape2(a, "a")
-    N = _shape2(b, "b")[0]
-    dt = _float_code(out, "out")
-    ld_a, ld_b = _code_rows(a, "a", (R, K)), _code_rows(b, "b", (N, K))
-    KB = -(-K // 128)
-    ld_s = _rows_of(a_scale, "a_scale", (torch.float32,), (KB, R))
-    _check_tensor(b_scale, "b_scale", (torch.float32,), (-(-N // 128), KB))
-    ld_o = _rows_of(out, "out", (out.dtype,), (R, N))
-    _check_status(status)
-    _run(lib.moe_fp8_matmul, "moe_fp8_matmul",
-         (("a", a), ("a_scale", a_scale), ("b", b), ("b_scale", b_scale), ("out", out), ("status", status)),
-         (a.data_ptr(), ld_a, a_scale.data_ptr(), ld_s, R, b.data_ptr(), ld_b, b_scale.data_ptr(), N, K, out.data_ptr(),
-          dt, ld_o, _ptr(status)), stream)
-
-
-def moe_fp8_grouped_matmul(a, a_scale, b, b_scale, offsets, out, status=None, stream=None):
-    """The product of moe_fp8_matmul per expert: rows [offsets[g], offsets[g + 1]) of a by
-    matrix g of b [G, N, K] (b_scale [G, ceil(N / 128), ceil(K / 128)]); offsets int32
-    [G + 1] as moe_expert_plan writes them.  Rows outside every group keep their out."""
-    import torch
-    R, K = _shape2(a, "a")
-    if len(getattr(b, "shape", ())) != 3:
-        raise ValueError(f"b must be 3-D, not of shape {tuple(getattr(b, 'shape', ()))}")
-    G, N = b.shape[:2]
-    dt = _float_code(out, "out")
-    ld_a, ld_b = _code_rows(a, "a", (R, K)), _code_rows(b, "b", (G, N, K))
-    KB = -(-K // 128)
-    ld_s = _rows_of(a_scale, "a_scale", (torch.float32,), (KB, R))
-    _check_tensor(b_scale, "b_scale", (torch.float32,), (G, -(-N // 128), KB))
-    _check_tensor(offsets, "offsets", (torch.int32,), (G + 1,))
-    ld_o = _rows_of(out, "out", (out.dtype,), (R, N))
-    _check_status(status)
-    _run(lib.moe_fp8_grouped_matmul, "moe_fp8_grouped_matmul",
-         (("a", a), ("a_scale", a_scale), ("b", b), ("b_scale", b_scale), ("offsets", offsets), ("out", out),
-          ("status", status)),
-         (a.data_ptr(), ld_a, a_scale.data_ptr(), ld_s, R, b.data_ptr(), ld_b, b.stride(0) if G > 1 else 0,
-          b_scale.data_ptr(), offsets.data_ptr(), G, N, K, out.data_ptr(), dt, ld_o, _ptr(status)), stream)
-
-
 def pack_layer(li, max_tokens=64, max_top_k=None, device=0, flags=0, expert_window=None, shared=True):
     """Pack a synth.LayerInputs-like object (router, gate_up, down, scales, table).
     expert_window=(begin, end) packs only those routed experts (and the shared
@@ -671,3 +433,22 @@ def pack_layer(li, max_tokens=64, max_top_k=None, device=0, flags=0, expert_wind
                             li.down[E] if has_sh else None, max_tokens,
                             max_top_k if max_top_k is not None else wl.top_k, device, flags,
                             None if expert_window is None else (b, e))
+
+
+# The operators beside the layer (operators.py) are part of this namespace; they
+# need torch at import, which the rest of the package does not.
+_OPERATORS = ("moe_expert_plan", "moe_balance_loss_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward",
+              "moe_fp8_quantize", "moe_fp8_quantize_weight", "moe_fp8_matmul", "moe_fp8_grouped_matmul")
+
+
+def __getattr__(name):
+    if name in _OPERATORS:
+        from . import operators
+        for n in _OPERATORS:
+            globals()[n] = getattr(operators, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted(set(globals()) | set(_OPERATORS))
