@@ -29,12 +29,15 @@ constexpr float kE4m3Max = 448.f;
 constexpr float kAmaxFloor = 448.f * 1.17549435e-38f;  // 448 * 2^-126
 constexpr int kQuantThreads = 256, kQuantRows = 8;
 
-__device__ __forceinline__ void block_scale(uint32_t amax_bits, float &scale, float &inv)
+// scale = a / 448 and inv = 448 / a, both correctly rounded.  The division by a constant is
+// Markstein's (IBM J. Res. Dev. 34, 1990): with c the rounded 1 / 448 and q = a c, one
+// exact residual corrects q to the rounded quotient; an infinite a is left as it is.
+__device__ __forceinline__ void block_scale(float amax, float &scale, float &inv)
 {
-    // amax as bits of |x|: integer order puts NaN above infinity, so it survives
-    float a = __uint_as_float(amax_bits);
-    a = a < kAmaxFloor ? kAmaxFloor : a;
-    scale = __fdiv_rn(a, kE4m3Max);
+    const float a = amax < kAmaxFloor ? kAmaxFloor : amax;  // NaN stays
+    constexpr float c = 1.f / kE4m3Max;
+    const float q = a * c;
+    scale = a == INFINITY ? a : __fmaf_rn(__fmaf_rn(-q, kE4m3Max, a), c, q);
     inv = __fdiv_rn(kE4m3Max, a);
 }
 
@@ -46,29 +49,61 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
     return r;
 }
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// largest magnitude of three values; NaN if one is
+__device__ __forceinline__ float amax3(float a, float b, float c)
+{
+    float m;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
 
-__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + expf(-g)); }
+__device__ __forceinline__ float amax8(const float (&v)[8])
+{
+    return amax3(amax3(v[0], v[1], v[2]), amax3(v[3], v[4], v[5]), amax3(v[6], v[7], 0.f));
+}
 
+__device__ __forceinline__ float amax2(float a, float b) { return amax3(a, b, 0.f); }
+
+// g / (1 + exp(-g)) from the hardware's 2^t and reciprocal (2^-22 relative each); t = -g log2(e)
+// is rounded, which adds |g| 2^-24 for negative g.  A sigmoid below 2^-126 is 0.
+__device__ __forceinline__ float silu(float g)
+{
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return g * r;
+}
+
+// Eight values as loaded, and as fp32.
 template <class T>
-__device__ __forceinline__ void load8(const T *p, float (&v)[8]);
+struct Raw8;
 template <>
-__device__ __forceinline__ void load8<float>(const float *p, float (&v)[8])
-{
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, float (&v)[8])
-{
-    const uint4 r = __ldg(reinterpret_cast<const uint4 *>(p));
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p)
+    {
+        a = __ldg(reinterpret_cast<const float4 *>(p));
+        b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
     }
-}
+    __device__ __forceinline__ void values(float (&v)[8]) const
+    {
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+};
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 r;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { r = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void values(float (&v)[8]) const
+    {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
 
 __device__ __forceinline__ float as_float(float v) { return v; }
 __device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -89,12 +124,55 @@ template <class T, bool WIDE>
 __device__ __forceinline__ void load_values(const T *row, int c0, int cols, float (&v)[8])
 {
     if (WIDE && c0 + 8 <= cols) {
-        load8<T>(row + c0, v);
+        Raw8<T> r;
+        r.load(row + c0);
+        r.values(v);
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = c0 + j < cols ? as_float(row[c0 + j]) : 0.f;
     }
 }
+
+// the same of a source row, or of its SwiGLU; zeros for no row
+template <class T, bool SWIGLU, bool WIDE>
+__device__ __forceinline__ void row_values(const T *x, int c0, int cols, float (&v)[8])
+{
+    if (!x) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+        return;
+    }
+    load_values<T, WIDE>(x, c0, cols, v);
+    if (SWIGLU) {
+        float w[8];
+        load_values<T, WIDE>(x + cols, c0, cols, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = silu(v[j]) * w[j];
+    }
+}
+
+// the lane's eight values of block b of `row`
+__device__ __forceinline__ void store_codes(const QuantArgs &a, const float (&v)[8], float inv, int row, int b, int lane)
+{
+    uint2 q;
+    q.x = e4m3x2(v[0] * inv, v[1] * inv) | e4m3x2(v[2] * inv, v[3] * inv) << 16;
+    q.y = e4m3x2(v[4] * inv, v[5] * inv) | e4m3x2(v[6] * inv, v[7] * inv) << 16;
+    const int c0 = b * kScaleBlock + lane * 8;
+    uint8_t *dst = a.codes + (int64_t)row * a.ld_codes + c0;
+    if (c0 + 8 <= a.cols) {
+        *reinterpret_cast<uint2 *>(dst) = q;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c0 + j < a.cols) dst[j] = (uint8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+    }
+}
+
+// Two blocks of a row at a time: all their loads first, and one sequence of shuffles and
+// divisions for both (lanes 0-7 of the half-warp end up with the first block's maximum,
+// lanes 8-15 with the second's).  The kernel is bound by instruction issue on bf16.
+constexpr int kQuantPer = kQuantThreads / 16 / kQuantRows;  // half-warps on a row
+constexpr int kQuantTurn = 2 * kQuantPer;                   // blocks of a row a CTA takes at a time
 
 template <class T, bool SWIGLU, bool WIDE>
 __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const QuantArgs a)
@@ -106,42 +184,49 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const Quan
         const int src = a.index ? __ldg(a.index + row) : row;
         if ((unsigned)src < (unsigned)a.src_rows) x = static_cast<const T *>(a.x) + (int64_t)src * a.ld_x;
     }
-    const int per = kQuantThreads / 16 / kQuantRows;  // blocks of a row in flight
-    for (int b = half / kQuantRows + blockIdx.y * per; b < a.blocks; b += per * gridDim.y) {
-        const int c0 = b * kScaleBlock + lane * 8;
-        float v[8];
-        if (x) {
-            load_values<T, WIDE>(x, c0, a.cols, v);
+    for (int b0 = half / kQuantRows + blockIdx.y * kQuantTurn; b0 < a.blocks; b0 += kQuantTurn * gridDim.y) {
+        const int b1 = b0 + kQuantPer;
+        float v0[8], v1[8];
+        if (WIDE && (b1 + 1) * kScaleBlock <= a.cols) {
+            Raw8<T> g0 = {}, g1 = {}, u0 = {}, u1 = {};
+            if (x) {
+                const T *p0 = x + b0 * kScaleBlock + lane * 8, *p1 = p0 + kQuantPer * kScaleBlock;
+                g0.load(p0);
+                g1.load(p1);
+                if (SWIGLU) {
+                    u0.load(p0 + a.cols);
+                    u1.load(p1 + a.cols);
+                }
+            }
+            g0.values(v0);
+            g1.values(v1);
             if (SWIGLU) {
-                float u[8];
-                load_values<T, WIDE>(x + a.cols, c0, a.cols, u);
+                float w0[8], w1[8];
+                u0.values(w0);
+                u1.values(w1);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = silu(v[j]) * u[j];
+                for (int j = 0; j < 8; ++j) {
+                    v0[j] = silu(v0[j]) * w0[j];
+                    v1[j] = silu(v1[j]) * w1[j];
+                }
             }
         } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = 0.f;
+            row_values<T, SWIGLU, WIDE>(x, b0 * kScaleBlock + lane * 8, a.cols, v0);
+            row_values<T, SWIGLU, WIDE>(x, b1 * kScaleBlock + lane * 8, a.cols, v1);
         }
-        uint32_t m = 0;
+        const bool second = lane & 8;
+        const float m0 = amax8(v0), m1 = amax8(v1);
+        float m = amax2(second ? m1 : m0, __shfl_xor_sync(0xffffffffu, second ? m0 : m1, 8));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
-#pragma unroll
-        for (int d = 8; d; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+        for (int d = 4; d; d >>= 1) m = amax2(m, __shfl_xor_sync(0xffffffffu, m, d));
         float scale, inv;
         block_scale(m, scale, inv);
+        const float inv0 = __shfl_sync(0xffffffffu, inv, 0, 16), inv1 = __shfl_sync(0xffffffffu, inv, 8, 16);
         if (row >= a.rows) continue;
-        uint2 q;
-        q.x = e4m3x2(v[0] * inv, v[1] * inv) | e4m3x2(v[2] * inv, v[3] * inv) << 16;
-        q.y = e4m3x2(v[4] * inv, v[5] * inv) | e4m3x2(v[6] * inv, v[7] * inv) << 16;
-        uint8_t *dst = a.codes + (int64_t)row * a.ld_codes + c0;
-        if (c0 + 8 <= a.cols) {
-            *reinterpret_cast<uint2 *>(dst) = q;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c0 + j < a.cols) dst[j] = (uint8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
-        }
-        if (lane == 0) a.scales[(int64_t)b * a.ld_scales + row] = scale;
+        store_codes(a, v0, inv0, row, b0, lane);
+        if (b1 < a.blocks) store_codes(a, v1, inv1, row, b1, lane);
+        const int b = second ? b1 : b0;
+        if ((lane & 7) == 0 && b < a.blocks) a.scales[(int64_t)b * a.ld_scales + row] = scale;
     }
 }
 
@@ -152,13 +237,13 @@ __global__ void __launch_bounds__(kQuantThreads)
                            uint8_t *__restrict__ codes, int64_t ld_codes, int64_t codes_stride,
                            float *__restrict__ scales)
 {
-    __shared__ uint32_t red[kQuantThreads / 32];
+    __shared__ float red[kQuantThreads / 32];
     const int kb = blockIdx.x, nb = blockIdx.y, g = blockIdx.z;
     const int c0 = kb * kScaleBlock + (threadIdx.x & 15) * 8;
     const int r0 = nb * kScaleBlock + (threadIdx.x >> 4);
     const T *src = w + (int64_t)g * group_stride;
     float v[8][8];
-    uint32_t m = 0;
+    float m = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int r = r0 + 16 * i;
@@ -168,14 +253,14 @@ __global__ void __launch_bounds__(kQuantThreads)
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[i][j]));
+        m = amax2(m, amax8(v[i]));
     }
-    m = __reduce_max_sync(0xffffffffu, m);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = amax2(m, __shfl_xor_sync(0xffffffffu, m, d));
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kQuantThreads / 32; ++i) m = max(m, red[i]);
+    for (int i = 0; i < kQuantThreads / 32; ++i) m = amax2(m, red[i]);
     float scale, inv;
     block_scale(m, scale, inv);
     if (threadIdx.x == 0) scales[((int64_t)g * gridDim.y + nb) * gridDim.x + kb] = scale;
@@ -242,8 +327,8 @@ extern "C" moe_status moe_fp8_quantize(const void *x, moe_dtype x_dtype, int64_t
     const bool wide = aligned(x, 16) && ld_x * size % 16 == 0 && (!swiglu || (int64_t)cols * size % 16 == 0);
     QuantKernel f = x_dtype == MOE_DT_BF16 ? quant_pick<__nv_bfloat16>(swiglu, wide) : quant_pick<float>(swiglu, wide);
     const int row_ctas = ceil_div(n_rows, kQuantRows);
-    // few rows: one CTA per pair of blocks; many: a CTA walks its rows' blocks
-    const int by = std::max(1, std::min(ceil_div(a.blocks, kQuantThreads / 16 / kQuantRows), 1184 / row_ctas));
+    // few rows: a CTA per turn of blocks; many: a CTA walks its rows' blocks
+    const int by = std::max(1, std::min(ceil_div(a.blocks, kQuantTurn), 1184 / row_ctas));
     f<<<dim3(row_ctas, by), kQuantThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
     return launched(cudaGetLastError());
 }
