@@ -33,7 +33,7 @@ using namespace op;
 constexpr int kBalWarps = 16, kBalThreads = 32 * kBalWarps;
 constexpr int kBalCluster = 8;      // CTAs of the cluster that adds the column sums
 constexpr int kBalMaxCtas = 148;    // CTAs with partial sums in the workspace
-constexpr int kBalRowsPerWarp = 2;  // below this many rows a warp, fewer CTAs
+constexpr int kBalOneLaunch = 128;  // tokens of one cluster, a row a warp (512 tokens, 512 experts: 9.9 us; two launches 7.4)
 
 // A lane's values of a row: NV of them, V consecutive at a time (16 bytes, or
 // one where rows are not 16-byte aligned); value (i, j) is column
@@ -111,13 +111,15 @@ __device__ __forceinline__ void row_softmax(float (&v)[NV])
     for (int i = 1; i < NV; ++i) m = fmaxf(m, v[i]);
 #pragma unroll
     for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    // fmaxf passes over NaN: those come back through exp(NaN - m) below; with
-    // m = -inf subtract 0 so that an empty row gives exp(-inf) = 0
-    const float shift = m == -INFINITY ? 0.f : m;
+    // fmaxf passes over NaN: those come back through 2^NaN below; with m = -inf subtract
+    // 0 so that an empty row gives 2^-inf = 0.  exp(l - m) = 2^(l log2(e) - m log2(e)) in one
+    // FMA: the rounding of m log2(e) is the same for the whole row and cancels.
+    constexpr float log2e = 1.44269504f;
+    const float shift = m == -INFINITY ? 0.f : -m * log2e;
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        v[i] = expf(v[i] - shift);
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[i]) : "f"(__fmaf_rn(v[i], log2e, shift)));
         s += v[i];
     }
 #pragma unroll
@@ -140,19 +142,23 @@ struct BalanceArgs {
 };
 
 // Column sums, counts and P, f, loss from the partial sums of `ctas` CTAs: the
-// cluster's CTA r owns columns [r * cols, (r + 1) * cols).  Partials lie in
-// the workspace, or in the cluster's shared memory (DSMEM).
+// cluster's CTA r owns columns [r * cols, (r + 1) * cols), at most 128 of them
+// where the cluster is full.  Partials lie in the workspace, or in the cluster's
+// shared memory (DSMEM, ctas = the cluster's size).
 template <bool DSMEM>
 __device__ void balance_reduce(const BalanceArgs &a, const float *s_sum, const int32_t *s_cnt, const int32_t *s_valid)
 {
-    __shared__ float red_p[kBalWarps][32];
-    __shared__ int32_t red_c[kBalWarps][32];
+    __shared__ float red_p[kBalThreads], warp_loss[4];
+    __shared__ int32_t red_c[kBalThreads];
     __shared__ int n_valid;
     __shared__ float loss_part;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned rank = cluster_rank(), ranks = cluster_size();
     const int cols = (int)((a.E + ranks - 1) / ranks);
     const int c0 = (int)rank * cols, c1 = min(a.E, c0 + cols);
+    // 32, 64 or 128 columns at a time, the CTAs' partials over the rest of the threads
+    const int shift = cols <= 32 ? 5 : cols <= 64 ? 6 : 7, width = 1 << shift, parts = kBalThreads >> shift;
+    const int part = threadIdx.x >> shift, col = threadIdx.x & (width - 1);
     const uint32_t sum_at = DSMEM ? static_cast<uint32_t>(__cvta_generic_to_shared(s_sum)) : 0;
     const uint32_t cnt_at = DSMEM ? static_cast<uint32_t>(__cvta_generic_to_shared(s_cnt)) : 0;
     const uint32_t valid_at = DSMEM ? static_cast<uint32_t>(__cvta_generic_to_shared(s_valid)) : 0;
@@ -164,54 +170,66 @@ __device__ void balance_reduce(const BalanceArgs &a, const float *s_sum, const i
         for (int d = 16; d; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
         if (lane == 0) n_valid = n;
     }
-    __syncthreads();
-    const int n = n_valid;
-    const float inv_n = 1.f / (float)max(n, 1);
-    const float to_share = (float)((double)a.E / ((double)a.k * (double)max(n, 1)));
     float loss = 0.f;
-    for (int cb = c0; cb < c1; cb += 32) {
-        const int c = cb + lane;
+    for (int cb = c0; cb < c1; cb += width) {
+        const int c = cb + col;
         float p = 0.f;
         int cnt = 0;
         if (c < c1) {
-            for (int g = warp; g < a.ctas; g += kBalWarps) {
-                if (DSMEM) {
-                    p += cluster_ld_f32(cluster_map(sum_at, g) + 4 * c);
-                    cnt += (int)cluster_ld_u32(cluster_map(cnt_at, g) + 4 * c);
-                } else {
-                    p += a.psum[(size_t)g * a.E + c];
-                    cnt += a.pcount[(size_t)g * a.E + c];
+            for (int g0 = part; g0 < a.ctas; g0 += 8 * parts) {
+                float x[8];
+                int y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int g = g0 + i * parts;
+                    x[i] = 0.f;
+                    y[i] = 0;
+                    if (g < a.ctas) {
+                        x[i] = DSMEM ? cluster_ld_f32(cluster_map(sum_at, g) + 4 * c) : a.psum[(size_t)g * a.E + c];
+                        y[i] = DSMEM ? (int)cluster_ld_u32(cluster_map(cnt_at, g) + 4 * c) : a.pcount[(size_t)g * a.E + c];
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    p += x[i];
+                    cnt += y[i];
                 }
             }
         }
-        red_p[warp][lane] = p;
-        red_c[warp][lane] = cnt;
+        red_p[threadIdx.x] = p;
+        red_c[threadIdx.x] = cnt;
         __syncthreads();
-        if (warp == 0 && c < c1) {
-            for (int w = 1; w < kBalWarps; ++w) {
-                p += red_p[w][lane];
-                cnt += red_c[w][lane];
+        if (part == 0 && c < c1) {
+            for (int w = 1; w < parts; ++w) {
+                p += red_p[(w << shift) + col];
+                cnt += red_c[(w << shift) + col];
             }
-            p *= inv_n;
+            const double n = (double)max(n_valid, 1);
+            p *= (float)(1.0 / n);
             a.prob_mean[c] = p;
             a.counts[c] = cnt;
-            loss += (float)cnt * to_share * p;
+            loss += (float)cnt * (float)((double)a.E / ((double)a.k * n)) * p;
         }
         __syncthreads();
     }
-    if (warp == 0) {
+    if (warp < 4) {
 #pragma unroll
         for (int d = 16; d; d >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, d);
-        if (lane == 0) loss_part = loss;
+        if (lane == 0) warp_loss[warp] = loss;
     }
+    __syncthreads();
+    if (threadIdx.x == 0) loss_part = (warp_loss[0] + warp_loss[1]) + (warp_loss[2] + warp_loss[3]);
     if (ranks > 1) cluster_sync();
     else __syncthreads();
     if (rank == 0 && threadIdx.x == 0) {
         const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(&loss_part));
-        float l = 0.f;
-        for (unsigned r = 0; r < ranks; ++r) l += ranks > 1 ? cluster_ld_f32(cluster_map(at, r)) : loss_part;
+        float x[kBalCluster], l = 0.f;
+#pragma unroll
+        for (unsigned r = 0; r < kBalCluster; ++r) x[r] = r < ranks ? (ranks > 1 ? cluster_ld_f32(cluster_map(at, r)) : loss_part) : 0.f;
+#pragma unroll
+        for (unsigned r = 0; r < kBalCluster; ++r) l += x[r];
         *a.loss = l;
-        a.counts[a.E] = n;
+        a.counts[a.E] = n_valid;
     }
     if (ranks > 1) cluster_sync();  // the other CTAs' shared memory is read until here
 }
@@ -227,6 +245,7 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_forward_kernel(const B
     __shared__ int32_t cta_valid;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const T *logits = static_cast<const T *>(a.logits);
+    if (!CLUSTER) dependents_launch();  // the second kernel may wait on the SMs
     for (int e = threadIdx.x; e < a.E; e += kBalThreads) hist[e] = 0;
     if (threadIdx.x == 0) cta_valid = 0;
     __syncthreads();
@@ -237,16 +256,27 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_forward_kernel(const B
     int n_valid = 0;
     const int step = gridDim.x * kBalWarps;
     int t = blockIdx.x * kBalWarps + warp;
+    // the next row's logits, mask and choices are in flight while this one is summed
     float next[NV];
-    if (t < a.T) load_row<T, NV, V>(logits + (size_t)t * a.E, a.E, lane, next);
+    int next_choice = -1;
+    bool next_valid = true;
+    const auto fetch = [&](int row) {
+        load_row<T, NV, V>(logits + (size_t)row * a.E, a.E, lane, next);
+        next_valid = !a.valid || __ldg(a.valid + row);
+        next_choice = lane < a.k ? __ldg(a.idx + (size_t)row * a.k + lane) : -1;
+    };
+    if (t < a.T) fetch(t);
     for (; t < a.T; t += step) {
         float v[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) v[i] = next[i];
-        if (t + step < a.T) load_row<T, NV, V>(logits + (size_t)(t + step) * a.E, a.E, lane, next);
-        if (a.valid && !a.valid[t]) continue;
+        const int choice = next_choice;
+        const bool counted = next_valid;
+        if (t + step < a.T) fetch(t + step);
+        if (!counted) continue;
         ++n_valid;
-        for (int j = lane; j < a.k; j += 32) {
+        if ((unsigned)choice < (unsigned)a.E) atomicAdd(&hist[choice], 1);
+        for (int j = 32 + lane; j < a.k; j += 32) {
             const int e = __ldg(a.idx + (size_t)t * a.k + j);
             if ((unsigned)e < (unsigned)a.E) atomicAdd(&hist[e], 1);
         }
@@ -280,7 +310,6 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_forward_kernel(const B
         balance_reduce<true>(a, cta_sum, hist, &cta_valid);
     } else {
         if (threadIdx.x == 0) a.pvalid[blockIdx.x] = cta_valid;
-        dependents_launch();
     }
 }
 
@@ -310,11 +339,11 @@ __global__ void __launch_bounds__(kBwdThreads)
             const int c = (i * 32 + lane) * V + j;
             f[i * V + j] = c < E ? (float)__ldg(counts + c) * to_share : 0.f;
         }
+    // (a row ahead in registers costs more warps than it hides: 30.6 against 46.4 us at 65,536 x 512)
     for (int t = blockIdx.x * kBwdWarps + warp; t < tokens; t += gridDim.x * kBwdWarps) {
         float v[NV];
-        const bool counted = !valid || valid[t];
-        if (counted) {
-            load_row<T, NV, V>(logits + (size_t)t * E, E, lane, v);
+        load_row<T, NV, V>(logits + (size_t)t * E, E, lane, v);  // not held up by the mask
+        if (!valid || __ldg(valid + t)) {
             row_softmax<NV>(v);
             float dot = 0.f;
 #pragma unroll
@@ -377,10 +406,12 @@ bool wide_rows(const void *p, const void *q, moe_dtype dt, int E)
     return aligned(p, 16) && aligned(q, 16) && E % (dt == MOE_DT_BF16 ? 8 : 4) == 0;
 }
 
-int forward_ctas(int T)
+// One cluster (as many CTAs as have rows, or columns to add up), or partial sums of every SM.
+int forward_ctas(int T, int E)
 {
-    const int n = std::max(1, std::min(kBalMaxCtas, ceil_div(T, kBalWarps * kBalRowsPerWarp)));
-    return n > kBalCluster ? n : n > 4 ? 8 : n > 2 ? 4 : n;  // a cluster of 1, 2, 4 or 8
+    if (T > kBalOneLaunch) return std::min(kBalMaxCtas, ceil_div(T, kBalWarps));
+    const int rows = ceil_div(T, kBalWarps), cols = ceil_div(E, 64), n = std::max(rows, cols);
+    return n > 4 ? 8 : n > 2 ? 4 : std::max(n, 1);
 }
 
 PerDevice g_balance;
@@ -414,7 +445,7 @@ using namespace moe;
 extern "C" size_t moe_balance_loss_workspace_bytes(int n_tokens, int n_experts)
 {
     if (n_tokens <= 0 || n_experts < 1 || n_experts > kMaxExperts) return 0;
-    const int ctas = forward_ctas(n_tokens);
+    const int ctas = forward_ctas(n_tokens, n_experts);
     return ctas <= kBalCluster ? 0 : (size_t)ctas * n_experts * 8 + (size_t)ctas * 4;
 }
 
@@ -440,7 +471,7 @@ extern "C" moe_status moe_balance_loss(const void *logits, moe_dtype dtype, cons
     a.T = n_tokens;
     a.E = n_experts;
     a.k = top_k;
-    a.ctas = forward_ctas(n_tokens);
+    a.ctas = forward_ctas(n_tokens, n_experts);
     a.counts = counts;
     a.prob_mean = prob_mean;
     a.loss = loss;

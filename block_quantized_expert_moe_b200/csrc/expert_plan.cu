@@ -8,15 +8,17 @@
 //
 // A counting sort in one launch of one thread-block cluster.  Every warp owns a
 // contiguous range of pairs and one row of a per-warp histogram in shared
-// memory; 32 pairs at a time, __match_any_sync groups the lanes that chose the
-// same expert, so a warp needs no atomics and the rank of a pair inside its
-// group is the number of lower lanes in it.  The histograms are scanned over
-// the CTA's warps, the CTAs' totals over the cluster (distributed shared
-// memory), the experts' totals over the block; a second pass over the same
-// pairs writes slots and rows.  No atomics anywhere: the order is that of the
-// definition, and no workspace has to be kept or cleared.
+// memory; 32 pairs at a time, ballots group the lanes that chose the same
+// expert, so a warp needs no atomics and the rank of a pair inside its
+// group is the number of lower lanes in it plus what the warp has counted
+// before.  The ranks wait in `slots` while the histograms are scanned over the
+// CTA's warps, the CTAs' totals over the cluster (distributed shared memory)
+// and the experts' totals over the block; a second pass adds each pair's base.
+// No atomics anywhere: the order is that of the definition, and no workspace
+// has to be kept or cleared.
 //
-// The work is latency: 12 bytes a pair (index read, slot and row written).
+// The work is latency: 12 bytes a pair (index read, slot and row written).  A
+// cluster of 16 CTAs takes prefill chunks, one CTA the decode batches.
 #include <algorithm>
 
 #include "op_common.cuh"
@@ -27,7 +29,9 @@ namespace {
 using namespace op;
 
 constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
-constexpr int kPlanBatch = 4;  // index loads in flight per lane
+constexpr int kPlanBatch = 8;  // index loads in flight per lane
+constexpr int kPlanPairsOfOne = 2560;  // 7.5 us with one CTA and with a cluster; more pairs take a cluster
+constexpr int kPlanCluster = 16;  // beyond the portable 8: checked when the kernel is prepared
 
 __device__ __forceinline__ int load_choice(const int32_t *idx, int p, int end, int E)
 {
@@ -35,8 +39,22 @@ __device__ __forceinline__ int load_choice(const int32_t *idx, int p, int end, i
     return (unsigned)e < (unsigned)E ? e : -1;
 }
 
+// The lanes that chose the same expert, from one ballot per bit of the expert's number.
+// (__match_any_sync takes time with every distinct value: 78 against 62 us at 65,536
+// tokens of 10 choices among 512.)
+__device__ __forceinline__ unsigned same_choice(int e, int bits)
+{
+    unsigned same = __ballot_sync(0xffffffffu, e >= 0);
+    for (int b = 0; b < bits; ++b) {
+        const bool one = (e >> b) & 1;
+        const unsigned ones = __ballot_sync(0xffffffffu, one);
+        same &= one ? ones : ~ones;
+    }
+    return same;
+}
+
 __global__ void __launch_bounds__(kPlanThreads, 1)
-    expert_plan_kernel(const int32_t *__restrict__ idx, int P, int k, int E, int warps, int32_t *__restrict__ counts,
+    expert_plan_kernel(const int32_t *__restrict__ idx, int P, int k, int E, int bits, int warps, int32_t *__restrict__ counts,
                        int32_t *__restrict__ offsets, int32_t *__restrict__ rows, int32_t *__restrict__ slots)
 {
     extern __shared__ int32_t smem[];
@@ -47,7 +65,14 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned rank = cluster_rank(), ctas = cluster_size();
 
-    for (int i = threadIdx.x; i < warps * E; i += kPlanThreads) hist[i] = 0;
+    const int words = warps * E;  // the histograms start on 16 bytes where E is a multiple of 2
+    if ((E & 1) == 0) {
+        int4 *h4 = reinterpret_cast<int4 *>(hist);
+        for (int i = threadIdx.x; i < words / 4; i += kPlanThreads) h4[i] = make_int4(0, 0, 0, 0);
+        if (threadIdx.x < (words & 3)) hist[(words & ~3) + threadIdx.x] = 0;
+    } else {
+        for (int i = threadIdx.x; i < words; i += kPlanThreads) hist[i] = 0;
+    }
     __syncthreads();
 
     const int n_warps = warps * (int)ctas;
@@ -62,9 +87,14 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
         for (int b = 0; b < kPlanBatch; ++b) e[b] = load_choice(idx, p0 + 32 * b + lane, end, E);
 #pragma unroll
         for (int b = 0; b < kPlanBatch; ++b) {
-            const unsigned same = __match_any_sync(0xffffffffu, e[b]);
-            if (e[b] >= 0 && lane == __ffs(same) - 1) own[e[b]] += __popc(same);
+            const int p = p0 + 32 * b + lane;
+            if (p0 + 32 * b >= end) break;
+            const unsigned same = same_choice(e[b], bits);
+            const int before = e[b] >= 0 ? own[e[b]] : 0;
             __syncwarp();
+            if (e[b] >= 0 && lane == __ffs(same) - 1) own[e[b]] = before + __popc(same);
+            __syncwarp();
+            if (p < end) slots[p] = before + __popc(same & ((1u << lane) - 1));
         }
     }
     __syncthreads();
@@ -72,10 +102,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     // over the CTA's warps: hist becomes the pairs of earlier warps
     for (int e = threadIdx.x; e < E; e += kPlanThreads) {
         int run = 0;
-        for (int w = 0; w < warps; ++w) {
-            const int n = hist[w * E + e];
-            hist[w * E + e] = run;
-            run += n;
+        for (int w0 = 0; w0 < warps; w0 += 8) {
+            int n[8];
+#pragma unroll
+            for (int w = 0; w < 8; ++w) n[w] = w0 + w < warps ? hist[(w0 + w) * E + e] : 0;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                if (w0 + w < warps) hist[(w0 + w) * E + e] = run;
+                run += n[w];
+            }
         }
         total[e] = run;
     }
@@ -87,10 +122,13 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     if (threadIdx.x < E) {
         if (ctas > 1) {
             const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(total + threadIdx.x));
-            for (unsigned c = 0; c < ctas; ++c) {
-                const int n = (int)cluster_ld_u32(cluster_map(a, c));
-                if (c < rank) before += n;
-                all += n;
+            int n[kPlanCluster];
+#pragma unroll
+            for (unsigned c = 0; c < kPlanCluster; ++c) n[c] = c < ctas ? (int)cluster_ld_u32(cluster_map(a, c)) : 0;
+#pragma unroll
+            for (unsigned c = 0; c < kPlanCluster; ++c) {
+                if (c < rank) before += n[c];
+                all += n[c];
             }
         } else {
             all = total[threadIdx.x];
@@ -127,22 +165,20 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     __syncthreads();
 
     for (int p0 = begin; p0 < end; p0 += 32 * kPlanBatch) {
-        int e[kPlanBatch];
-#pragma unroll
-        for (int b = 0; b < kPlanBatch; ++b) e[b] = load_choice(idx, p0 + 32 * b + lane, end, E);
+        int e[kPlanBatch], r[kPlanBatch];
 #pragma unroll
         for (int b = 0; b < kPlanBatch; ++b) {
             const int p = p0 + 32 * b + lane;
-            const unsigned same = __match_any_sync(0xffffffffu, e[b]);
-            int slot = -1;
-            if (e[b] >= 0) {
-                slot = base[e[b]] + own[e[b]] + __popc(same & ((1u << lane) - 1));
-                rows[slot] = p / k;
-            }
-            __syncwarp();
-            if (e[b] >= 0 && lane == __ffs(same) - 1) own[e[b]] += __popc(same);
-            __syncwarp();
-            if (p < end) slots[p] = slot;
+            e[b] = load_choice(idx, p, end, E);
+            r[b] = p < end ? slots[p] : 0;  // written by this lane above
+        }
+#pragma unroll
+        for (int b = 0; b < kPlanBatch; ++b) {
+            const int p = p0 + 32 * b + lane;
+            if (p >= end) continue;
+            const int slot = e[b] >= 0 ? base[e[b]] + own[e[b]] + r[b] : -1;
+            slots[p] = slot;
+            if (slot >= 0) rows[slot] = p / k;
         }
     }
     // rows behind the last group belong to no token
@@ -154,11 +190,34 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
 size_t plan_smem(int E, int warps) { return sizeof(int32_t) * (size_t)E * (2 + warps); }
 
 PerDevice g_plan;
+int g_plan_cluster[kMaxDevices];  // largest cluster of the device, 16 or 8
 
 cudaError_t plan_prepare()
 {
-    return cudaFuncSetAttribute(expert_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)plan_smem(kMaxExperts, kPlanWarps));
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(expert_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)plan_smem(kMaxExperts, kPlanWarps));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(expert_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = kPlanCluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(kPlanCluster);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = plan_smem(kMaxExperts, kPlanWarps);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int fit = 0;
+    if (cudaOccupancyMaxActiveClusters(&fit, expert_plan_kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        fit = 0;
+    }
+    g_plan_cluster[dev] = fit > 0 ? kPlanCluster : 8;
+    return cudaSuccess;
 }
 
 }  // namespace
@@ -181,8 +240,14 @@ extern "C" moe_status moe_expert_plan(const int32_t *idx, int n_tokens, int top_
     const moe_status st = g_plan.get(&sms, plan_prepare);
     if (st != MOE_OK) return st;
     const int warps = (int)std::min<int64_t>(kPlanWarps, std::max<int64_t>(1, (pairs + 31) / 32));
-    const int ctas = pairs > 32 * kPlanWarps * kPlanBatch ? 8 : 1;
+    int bits = 0, ctas = 1;
+    while ((1 << bits) < n_experts) ++bits;
+    if (pairs > kPlanPairsOfOne) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+        ctas = g_plan_cluster[dev];
+    }
     return launched(launch(expert_plan_kernel, dim3(ctas), kPlanThreads, plan_smem(n_experts, warps),
-                           static_cast<cudaStream_t>(stream), ctas, false, idx, (int)pairs, top_k, n_experts, warps,
+                           static_cast<cudaStream_t>(stream), ctas, false, idx, (int)pairs, top_k, n_experts, bits, warps,
                            counts, offsets, rows, slots));
 }
