@@ -46,13 +46,14 @@ struct Config {
     static constexpr int MIN_CTAS = MIN_CTAS_;
     static constexpr int COLS = BN * 4 / EPI;  // columns of an epilogue thread
     static constexpr int THREADS = 32 * (EPI + 3);
-    static constexpr int SCALES = 4;           // ring of scale rows
+    static constexpr int SCALES = 8;           // ring of scale rows
     static constexpr int STAGE_BYTES = kABytes + BN * 128;
     static constexpr int TABLE = 2 * (kMaxExperts + 1) * 4;  // group offsets, first tiles
     static constexpr int SMEM = STAGES * STAGE_BYTES + SCALES * BN * 4 + TABLE + 1024;
     static_assert(STAGES * STAGE_BYTES >= kWeightRows * BN * 4 || MIN_CTAS == 1, "partial tile fits the operand ring");
 };
 typedef Config<64, 4, 4, 4, 16, 2> Narrow;
+typedef Config<16, 5, 4, 4, 16, 2> Token;  // at most 16 rows: a deeper ring of smaller stages
 
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                        uint32_t accumulate)
@@ -91,6 +92,32 @@ __device__ __forceinline__ void fma_pair(float2 &acc, uint32_t v0, uint32_t v1, 
         "fma.rn.f32x2 ra, rv, rs, ra;\n\tmov.b64 {%0, %1}, ra;\n\t}"
         : "+f"(acc.x), "+f"(acc.y)
         : "r"(v0), "r"(v1), "f"(s0), "f"(s1));
+}
+
+// This rank's columns of the tile: the cluster's partial sums in rank order, 32 of them in
+// flight.
+template <class C, int RANKS, class OUT>
+__device__ __forceinline__ void add_partials(uint32_t own, int rank, int cols, OUT *out, int64_t ld)
+{
+    constexpr int STEP = RANKS * (C::EPI / 4), N = 32 / RANKS;
+#pragma unroll 1
+    for (int c0 = rank * (C::EPI / 4) + (threadIdx.x >> 7); c0 < cols; c0 += N * STEP) {
+        float p[N][RANKS];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int r = 0; r < RANKS; ++r) {
+                p[i][r] = 0.f;
+                if (c0 + i * STEP < cols) p[i][r] = cluster_ld_f32(cluster_map(own + (c0 + i * STEP) * kWeightRows * 4, r));
+            }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float v = p[i][0];
+#pragma unroll
+            for (int r = 1; r < RANKS; ++r) v += p[i][r];
+            if (c0 + i * STEP < cols) out[(int64_t)(c0 + i * STEP) * ld] = OUT(v);
+        }
+    }
 }
 
 template <class C, class OUT>
@@ -138,58 +165,65 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
     tc_fence_after_sync();
     const uint32_t tmem = tmem_base;
     const int n_work = first_tile[a.groups] * a.n_tiles;
-    const int worker = blockIdx.x / ranks, workers = gridDim.x / ranks;
-    const int kb0 = (int)((int64_t)a.kblocks * rank / ranks), kb1 = (int)((int64_t)a.kblocks * (rank + 1) / ranks);
+    const int shift = 31 - __clz(ranks);  // 1, 2, 4 or 8 ranks
+    const int worker = blockIdx.x >> shift, workers = gridDim.x >> shift;
+    const int kb0 = (int)((int64_t)a.kblocks * rank >> shift), kb1 = (int)((int64_t)a.kblocks * (rank + 1) >> shift);
     int issued = 0;
 
-    // One tile of each role; a timed-out wait sets abort_flag, after which the
-    // roles skip their work but still meet at the cluster's barriers.
-    int it = 0, sit = 0;  // this role's position in the operand ring / the block sequence
-    for (int id = worker; id < n_work; id += workers) {
-        const Tile t = tile_at(id, a.n_tiles, a.groups, first_tile, offset);
+    // One tile of each role; after a wait that ran out a warp skips its work (and the others'
+    // waits run out) but still meets the cluster's barriers.
+    Ring<C::STAGES> ring;  // this warp's positions
+    Ring<C::BUFS> buf;
+    Ring<C::SCALES> scale;
+    bool go = true;
+    TileWalk walk(worker, workers, a.n_tiles);
+    for (int id = worker; id < n_work; id += workers, walk.next()) {
+        const Tile t = walk.tile(a.groups, first_tile, offset);
         const int ncols = (max(t.rows, 1) + 15) & ~15;
         float2 acc[C::COLS / 2];
+        // (the issuing warps run converged and one lane issues: in a branch of one lane descriptors
+        // do not count as uniform, and each instruction costs a sequence of moves)
         if (warp == C::EPI) {  // ---- TMA producer
-            if (lane == 0) {
-                const int boxes = (ncols + C::BOX - 1) / C::BOX;
-                for (int kb = kb0; kb < kb1 && !abort_flag; ++kb, ++it) {
-                    const int s = it % C::STAGES, u = it / C::STAGES;
-                    if (u > 0 && !mbar_wait(&empty[s], (u - 1) & 1)) {
-                        abort_flag = 1;
-                        break;
-                    }
-                    uint8_t *w_s = smem + s * C::STAGE_BYTES, *x_s = w_s + kABytes;
-                    mbar_arrive_expect_tx(&full[s], kABytes + boxes * C::BOX * 128);
-                    tma_load_3d(w_s, &map_w, &full[s], kb * 128, t.n_tile * kWeightRows, t.group);
+            const int boxes = (ncols + C::BOX - 1) / C::BOX;
+            for (int kb = kb0; kb < kb1 && go; ++kb) {
+                go = __all_sync(0xffffffffu, bar_wait(smem_u32(empty) + 8 * ring.slot, ring.phase ^ 1));
+                if (!go) break;
+                if (elect_one()) {
+                    uint8_t *w_s = smem + ring.slot * C::STAGE_BYTES, *x_s = w_s + kABytes;
+                    uint64_t *bar = &full[ring.slot];
+                    mbar_arrive_expect_tx(bar, kABytes + boxes * C::BOX * 128);
+                    tma_load_3d(w_s, &map_w, bar, kb * 128, t.n_tile * kWeightRows, t.group);
                     for (int b = 0; b < boxes; ++b)
-                        tma_load_2d(x_s + b * C::BOX * 128, &map_x, &full[s], kb * 128, t.row0 + b * C::BOX);
+                        tma_load_2d(x_s + b * C::BOX * 128, &map_x, bar, kb * 128, t.row0 + b * C::BOX);
                 }
-                issued = it;
+                __syncwarp();
+                ++issued;
+                ring.next();
             }
         } else if (warp == C::EPI + 1) {  // ---- MMA issuer
-            if (lane == 0) {
-                const uint32_t idesc = idesc_e4m3(kWeightRows, ncols);
-                for (int kb = kb0; kb < kb1 && !abort_flag; ++kb, ++it) {
-                    const int s = it % C::STAGES, u = it / C::STAGES;
-                    const int d = it % C::BUFS, du = it / C::BUFS;
-                    if ((du > 0 && !mbar_wait(&acc_empty[d], (du - 1) & 1)) || !mbar_wait(&full[s], u & 1)) {
-                        abort_flag = 1;
-                        break;
-                    }
-                    tc_fence_after_sync();
-                    const uint64_t wd = desc_kmajor_sw128(smem + s * C::STAGE_BYTES);
-                    const uint64_t xd = desc_kmajor_sw128(smem + s * C::STAGE_BYTES + kABytes);
+            const uint32_t idesc = idesc_e4m3(kWeightRows, ncols);
+            for (int kb = kb0; kb < kb1 && go; ++kb) {
+                const bool ok = bar_wait(smem_u32(full) + 8 * ring.slot, ring.phase) &&
+                                bar_wait(smem_u32(acc_empty) + 8 * buf.slot, buf.phase ^ 1);
+                go = __all_sync(0xffffffffu, ok);
+                if (!go) break;
+                tc_fence_after_sync();
+                if (elect_one()) {
+                    const uint64_t step = (uint64_t)(ring.slot * (C::STAGE_BYTES >> 4));
+                    const uint64_t wd = desc_kmajor_sw128(smem) + step, xd = desc_kmajor_sw128(smem + kABytes) + step;
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) mma_f8(tmem + d * C::BN, wd + 2 * kk, xd + 2 * kk, idesc, kk != 0);
-                    mma_commit(&empty[s]);
-                    mma_commit(&acc_full[d]);
+                    for (int kk = 0; kk < 4; ++kk) mma_f8(tmem + buf.slot * C::BN, wd + 2 * kk, xd + 2 * kk, idesc, kk != 0);
+                    mma_commit(&empty[ring.slot]);
+                    mma_commit(&acc_full[buf.slot]);
                 }
+                __syncwarp();
+                ring.next();
+                buf.next();
             }
         } else if (warp == C::EPI + 2) {  // ---- scales
             constexpr int PER = (C::BN + 31) / 32;  // columns of a lane
-            constexpr int AHEAD = 16 / PER > 4 ? 4 : 16 / PER;
+            constexpr int AHEAD = PER == 1 ? 8 : 4;  // blocks of loads in flight
             const float *bs = a.b_scale + ((int64_t)t.group * a.n_tiles + t.n_tile) * a.kblocks;
-            bool go = true;
             for (int k0 = kb0; k0 < kb1 && go; k0 += AHEAD) {
                 // every load from a valid address, so that none waits behind a branch
                 float v[AHEAD][PER], w[AHEAD];
@@ -204,14 +238,10 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i) {
                     if (k0 + i >= kb1) break;
-                    const int s = sit % C::SCALES, u = sit / C::SCALES;
-                    ++sit;
-                    if (lane == 0) {
-                        go = !abort_flag && (u == 0 || mbar_wait(&sc_empty[s], (u - 1) & 1));
-                        if (!go) abort_flag = 1;
-                    }
-                    go = __shfl_sync(0xffffffffu, go, 0);
+                    const int s = scale.slot;
+                    go = __all_sync(0xffffffffu, bar_wait(smem_u32(sc_empty) + 8 * s, scale.phase ^ 1));
                     if (!go) break;
+                    scale.next();
 #pragma unroll
                     for (int j = 0; j < PER; ++j)
                         if (j * 32 + lane < C::BN) scale_ring[s * C::BN + j * 32 + lane] = v[i][j] * w[i];
@@ -223,15 +253,18 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
             const int part = warp >> 2, c0 = part * C::COLS;
 #pragma unroll
             for (int i = 0; i < C::COLS / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const int d = it % C::BUFS, s = it % C::SCALES;
-                const bool ok = !abort_flag && mbar_wait(&acc_full[d], (it / C::BUFS) & 1) &&
-                                mbar_wait(&sc_full[s], (it / C::SCALES) & 1);
-                tc_fence_after_sync();
-                if (!__all_sync(0xffffffffu, ok)) {
-                    abort_flag = 1;
-                    break;
+            for (int kb = kb0; kb < kb1 && go; ++kb) {
+                const int d = buf.slot, s = scale.slot;
+                const uint32_t sc_at = smem_u32(sc_full) + 8 * s, acc_at = smem_u32(acc_full) + 8 * d;
+                const bool sc_ready = bar_try(sc_at, scale.phase), acc_ready = bar_try(acc_at, buf.phase);
+                if (!__all_sync(0xffffffffu, sc_ready && acc_ready)) {
+                    const bool ok = bar_wait(sc_at, scale.phase) && bar_wait(acc_at, buf.phase);
+                    go = __all_sync(0xffffffffu, ok);
+                    if (!go) break;
                 }
+                buf.next();
+                scale.next();
+                tc_fence_after_sync();
                 const uint32_t td = tmem + d * C::BN + c0 + ((uint32_t)((warp & 3) * 32) << 16);
                 const float *sc = scale_ring + s * C::BN + c0;
 #pragma unroll
@@ -257,6 +290,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
             }
         }
         __syncwarp();
+        if (!go) abort_flag = 1;
         if (ranks > 1) {
             // partial sums of the cluster's CTAs, added in rank order; the operand ring is
             // idle here (its last block has been multiplied) and holds this CTA's partial
@@ -274,15 +308,12 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
             cluster_sync();
             if (warp < C::EPI && !abort_flag) {
                 const int n = t.n_tile * kWeightRows + (threadIdx.x & 127);
-                for (int c = (int)rank * (C::EPI / 4) + (threadIdx.x >> 7); c < t.rows; c += ranks * (C::EPI / 4)) {
-                    const uint32_t at = smem_u32(partial + c * kWeightRows + (threadIdx.x & 127));
-                    float p[8], v = 0.f;
-#pragma unroll
-                    for (unsigned r = 0; r < 8; ++r) p[r] = r < ranks ? cluster_ld_f32(cluster_map(at, r)) : 0.f;
-#pragma unroll
-                    for (unsigned r = 0; r < 8; ++r) v += p[r];
-                    if (n < a.n) static_cast<OUT *>(a.out)[(int64_t)(t.row0 + c) * a.ld_out + n] = OUT(v);
-                }
+                OUT *out = static_cast<OUT *>(a.out) + (int64_t)t.row0 * a.ld_out + n;
+                const uint32_t own = smem_u32(partial + (threadIdx.x & 127));
+                const int cols = n < a.n ? t.rows : 0;
+                if (ranks == 2) add_partials<C, 2>(own, (int)rank, cols, out, a.ld_out);
+                else if (ranks == 4) add_partials<C, 4>(own, (int)rank, cols, out, a.ld_out);
+                else add_partials<C, 8>(own, (int)rank, cols, out, a.ld_out);
             }
             fence_proxy_async_smem();  // the ring is written by TMA again
             cluster_sync();
@@ -301,7 +332,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
     // after a timed-out wait: let copies and MMAs in flight land before memory is released
     if (abort_flag) {
         if (warp == C::EPI && lane == 0) drain_ring(full, C::STAGES, issued);
-        if (warp == C::EPI + 1 && lane == 0) drain_mma(&drain_bar);
+        if (warp == C::EPI + 1 && elect_one()) drain_mma(&drain_bar);
         if (threadIdx.x == 0 && a.status) atomicExch(a.status, (int)MOE_ERR_TIMEOUT);
     }
     tc_fence_before_sync();
@@ -337,7 +368,8 @@ PerDevice g_product;
 cudaError_t product_prepare()
 {
     if (!tmaps::encode_fn()) return cudaErrorUnknown;
-    const cudaError_t e = set_smem<Narrow>();
+    cudaError_t e = set_smem<Narrow>();
+    if (e == cudaSuccess) e = set_smem<Token>();
     return e != cudaSuccess ? e : pair_prepare();
 }
 
@@ -387,8 +419,11 @@ moe_status product(const uint8_t *a, int64_t ld_a, const float *a_scale, int64_t
     const int64_t narrow = most_tiles(Narrow::BN);
     const int slots = 2 * sms;
     int ranks = 1;
-    while (ranks < 8 && narrow * ranks * 2 <= slots && ranks * 2 <= p.kblocks) ranks *= 2;
-    return run_product<Narrow>(o, p, out_dtype, (int)std::min<int64_t>(narrow, slots / ranks), ranks, s);
+    const bool token = rows <= Token::BN;
+    while (ranks < 8 && narrow * ranks * 2 <= (token ? slots : sms) && ranks * 2 <= p.kblocks) ranks *= 2;
+    const int workers = (int)std::min<int64_t>(narrow, slots / ranks);
+    return token ? run_product<Token>(o, p, out_dtype, workers, ranks, s)
+                             : run_product<Narrow>(o, p, out_dtype, workers, ranks, s);
 }
 
 }  // namespace

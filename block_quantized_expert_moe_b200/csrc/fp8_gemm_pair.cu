@@ -46,51 +46,6 @@ constexpr int kPairSmem =
 constexpr int kEpilogueRegs = 216, kOtherRegs = 72;
 static_assert(32 * kEpiWarps * kEpilogueRegs + 128 * kOtherRegs <= kPairThreads * 168, "register split exceeds the launch's");
 
-// ---- shared memory by 32-bit addresses --------------------------------------------------
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity)
-{
-    if (bar_try(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (!bar_try(bar, parity))
-        if (clock64() - t0 > (1ll << 31)) return false;
-    return true;
-}
-
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t one;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
-    return one != 0;
-}
-
-// Position in a ring of N barriers: slot and the parity of its current use.
-template <int N>
-struct Ring {
-    int slot = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void next()
-    {
-        if (++slot == N) {
-            slot = 0;
-            phase ^= 1;
-        }
-    }
-};
-
 // ---- cta_group::2 forms ------------------------------------------------------------
 __device__ __forceinline__ void tmem_alloc2(uint32_t *dst, uint32_t ncols)
 {
@@ -270,51 +225,6 @@ __device__ __forceinline__ void store_row(OUT *out, const float (&acc)[kPart], i
 // multiple of 16.
 __device__ __forceinline__ int cta_rows(int rows) { return (rows + 1) / 2; }
 __device__ __forceinline__ int tile_columns(int left) { return left >= kPairWeights ? kPairWeights : (left + 15) & ~15; }
-
-// A warp's walk over its tiles (id, id + workers, ...): weight tile and token tile advance without
-// a division, the group by a search of 32 at a time from the last one.
-struct TileWalk {
-    int token_tile, n_tile, group, step_token, step_n, n_tiles;
-    __device__ __forceinline__ TileWalk(int id, int workers, int n_tiles_)
-        : token_tile(id / n_tiles_), n_tile(id % n_tiles_), group(0), step_token(workers / n_tiles_),
-          step_n(workers % n_tiles_), n_tiles(n_tiles_)
-    {
-    }
-    __device__ __forceinline__ void next()
-    {
-        token_tile += step_token;
-        n_tile += step_n;
-        if (n_tile >= n_tiles) {
-            n_tile -= n_tiles;
-            ++token_tile;
-        }
-    }
-    // the whole warp, converged
-    __device__ __forceinline__ Tile tile(int groups, const int *first_tile, const int *offset)
-    {
-        const int lane = threadIdx.x & 31;
-        for (;;) {  // groups whose successor starts at or before this token tile
-            const int g = group + lane;
-            const unsigned passed = __ballot_sync(0xffffffffu, g < groups - 1 && first_tile[min(g, groups - 1) + 1] <= token_tile);
-            group += __popc(passed);
-            if (passed != 0xffffffffu) break;
-        }
-        Tile t;
-        t.group = group;
-        t.n_tile = n_tile;
-        const int first = first_tile[group], parts = first_tile[group + 1] - first;
-        const int lo = offset[group], rows = offset[group + 1] - lo;
-        if (parts == 1) {
-            t.row0 = lo;
-            t.rows = rows;
-        } else {
-            const int size = (((rows + parts - 1) / parts) + 15) & ~15;
-            t.row0 = lo + (token_tile - first) * size;
-            t.rows = min(size, lo + rows - t.row0);
-        }
-        return t;
-    }
-};
 
 // WIDE: output rows start on 16-byte boundaries (map_y is then a map of the output).
 template <class OUT, bool WIDE>
