@@ -7,8 +7,8 @@
 #include <algorithm>
 
 #include "op_common.cuh"
-#include "tc_common.cuh"
-#include "tma_maps.cuh"
+#include "../tc_common.cuh"
+#include "../tma_maps.cuh"
 
 namespace moe {
 namespace fp8 {

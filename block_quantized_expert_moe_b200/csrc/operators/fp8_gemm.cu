@@ -414,16 +414,32 @@ moe_status product(const uint8_t *a, int64_t ld_a, const float *a_scale, int64_t
     };
     if (most_tiles(Narrow::BN) > INT32_MAX) return MOE_ERR_INVALID_ARG;
     const int64_t wide = most_tiles(kPairTokens) / p.n_tiles * ceil_div(n, 2 * kWeightRows);
-    const bool few_rows = (int64_t)rows <= 32ll * groups || wide < sms / 2;
-    if (!few_rows) return pair_product(o, p, out_dtype, (int)std::min<int64_t>(wide, sms / 2), s);
     const int64_t narrow = most_tiles(Narrow::BN);
-    const int slots = 2 * sms;
-    int ranks = 1;
+    const int slots = 2 * sms, pairs = sms / 2;
     const bool token = rows <= Token::BN;
+    // few tiles: split each one's K blocks over a cluster
+    int ranks = 1;
     while (ranks < 8 && narrow * ranks * 2 <= (token ? slots : sms) && ranks * 2 <= p.kblocks) ranks *= 2;
+    // The pair kernel, or this one.  Many waves of tiles: by the rows a group has on average, since
+    // both read every weight once (128 experts of 1024 x 2048, pair against narrow: 32 rows 73.1 /
+    // 59.9 us, 48 rows 74.8 / 68.0, 64 rows 76.4 / 76.7, 128 rows 88.4 / 123.7; 512 experts of 2048 x
+    // 512, 40 rows 188 / 168).  Few waves: by the blocks that the busiest CTA takes one after another,
+    // 0.5 us each for a pair, 0.65 us for a narrow tile alone on its SM and 0.9 us for two, and 2 us for
+    // a cluster's exchange (rows x n x k, pair / narrow: 128 x 4096 x 4096 17.8 / 15.7 us, 256 x 4096 x
+    // 4096 18.9 / 22.8, 1024 x 4096 x 4096 20.5 / 54.5, 256 x 1024 x 2048 12.1 / 8.9, 1024 x 1024 x 1024
+    // 9.1 / 10.3, 4096 x 512 x 512 7.6 / 10.4; 8 experts of 2048 x 2048, 64 rows 14.5 / 18.2).
+    bool pair = !token;
+    if (wide >= 4 * pairs) {
+        pair = pair && (int64_t)rows > 56ll * groups;
+    } else {
+        const int64_t pair_cost = 10 * (int64_t)p.kblocks * ceil_div(wide, pairs) + 20;  // in 50 ns
+        const int64_t each = (narrow * ranks > sms ? 18 : 13) * (int64_t)ceil_div(p.kblocks, ranks);
+        pair = pair && pair_cost < each * ceil_div(narrow * ranks, slots) + (ranks > 1 ? 40 : 0);
+    }
+    if (pair) return pair_product(o, p, out_dtype, (int)std::min<int64_t>(wide, pairs), s);
     const int workers = (int)std::min<int64_t>(narrow, slots / ranks);
     return token ? run_product<Token>(o, p, out_dtype, workers, ranks, s)
-                             : run_product<Narrow>(o, p, out_dtype, workers, ranks, s);
+                 : run_product<Narrow>(o, p, out_dtype, workers, ranks, s);
 }
 
 }  // namespace

@@ -8,7 +8,7 @@
 
 #include <mutex>
 
-#include "../../include/moe.h"
+#include "../../../include/moe.h"
 
 namespace moe {
 namespace op {

@@ -547,3 +547,125 @@ def test_operators_on_concurrent_streams():
     torch.cuda.synchronize()
     for l, (y, dl, loss) in zip(layers, want):
         assert torch.equal(l.y, y) and torch.equal(l.dlogits, dl) and torch.equal(l.loss, loss)
+
+
+# ---- sizes and buffers where the kernels' variants can go wrong ----------------------------
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("R,N,K", [(20001, 1, 256), (20000, 40, 512), (19000, 272, 128), (4096, 1504, 1152),
+                                   (257, 4096, 2048), (3, 75000, 200), (60, 20000, 130)])
+def test_product_of_extreme_shapes(R, N, K, dt):
+    a, sa, b, sb = operands(R, N, K, R + N)
+    out = torch.full((R, N), float("nan"), dtype=DTYPES[dt], device="cuda")
+    bq().moe_fp8_matmul(a, sa, b, sb, out)
+    check_product(out, a, sa, b, sb, K)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("counts,N", [([4000], 1000), ([300, 0, 700, 1, 130] * 6, 1000), ([9], 1000)])
+def test_products_leave_the_rest_of_a_wider_buffer(counts, N, dt):
+    """Rows on 16-byte boundaries in a wider buffer (whole tiles leave as boxes): columns behind n and rows
+    outside every group keep their values."""
+    K, first, behind = 300, 3, 40
+    R = first + sum(counts) + behind
+    a, sa, b, sb = operands(R, N, K, 21, len(counts))
+    wide = torch.randn(R, N + 24, device="cuda").to(DTYPES[dt])
+    before = wide.clone()
+    offsets = np.concatenate([[first], first + np.cumsum(counts)]).astype(np.int32)
+    bq().moe_fp8_grouped_matmul(a, sa, b, sb, torch.from_numpy(offsets).cuda(), wide[:, :N])
+    assert torch.equal(wide[:, N:], before[:, N:])
+    check_groups(wide[:, :N], before[:, :N], a, sa, b, sb, offsets, K)
+
+
+def test_products_beyond_32_bit_offsets():
+    """Outputs of more than 2^31 elements, weights and codes of more than 2^32 bytes: the last rows, the last
+    group and the last codes are right."""
+    R, N, K = 300000, 8192, 128
+    a, sa, b, sb = operands(R, N, K, 2)
+    out = torch.zeros(R, N, dtype=torch.bfloat16, device="cuda")
+    bq().moe_fp8_matmul(a, sa, b, sb, out)
+    check_product(out[-300:], a[-300:], sa[:, -300:], b, sb, K)
+    del out
+    G, N, K = 600, 1024, 8192
+    a, sa, b, sb = operands(40, N, K, 3)
+    weights = torch.zeros(G, N, K, dtype=torch.uint8, device="cuda")
+    weights[-1] = b
+    scales = torch.zeros(G, *sb.shape, device="cuda")
+    scales[-1] = sb
+    offsets = torch.zeros(G + 1, dtype=torch.int32, device="cuda")
+    offsets[-1] = 40
+    out = torch.zeros(40, N, device="cuda")
+    bq().moe_fp8_grouped_matmul(a, sa, weights, scales, offsets, out)
+    check_product(out, a, sa, b, sb, K)
+    del weights
+    R, C = 40000, 131072
+    x = torch.randn(3, C, generator=torch.Generator("cuda").manual_seed(1), device="cuda").bfloat16()
+    rows = torch.zeros(R, dtype=torch.int32, device="cuda")
+    rows[-1] = 2
+    codes, scales = torch.empty(R, C, dtype=torch.uint8, device="cuda"), torch.empty(C // 128, R, device="cuda")
+    bq().moe_fp8_quantize(x, codes, scales, rows=rows)
+    want, s = ref.quantize(x[2:].float().cpu().numpy())
+    assert same(values(codes[-1:]), want) and same(host(scales[:, -1:]), s.T.astype(np.float64))
+
+
+def test_quantize_scales_over_every_binade():
+    """The scale's division by 448 and its inverse, bit for bit, over mantissas of every exponent."""
+    rng = np.random.default_rng(4)
+    bits = (np.arange(1, 255, dtype=np.uint32)[:, None] << 23 | rng.integers(0, 1 << 23, (254, 128), dtype=np.uint32))
+    amax = bits.view(np.float32).reshape(-1)
+    x = np.zeros((amax.size, 128), np.float32)
+    x[:, 0], x[:, 1] = amax, -amax * np.float32(0.3)
+    codes, scales = run_quantize(torch.from_numpy(x).cuda(), *x.shape)
+    a = np.maximum(amax, ref.FLOOR)
+    s, inv = a / np.float32(448), np.float32(448) / a
+    assert np.array_equal(scales[0].cpu().numpy(), s)
+    got = values(codes)
+    assert np.array_equal(got[:, :2], ref.to_e4m3((x[:, :2] * inv[:, None]).astype(np.float64)))
+
+
+def test_balance_with_more_choices_than_a_warp():
+    g = torch.Generator(device="cuda").manual_seed(2)
+    logits = torch.randn(200, 70, generator=g, device="cuda")
+    check_balance(logits, logits.topk(50, 1).indices.int(), None)
+
+
+FIRST_CALLS = """
+import torch
+import block_quantized_expert_moe_b200 as bq
+x = torch.randn(300, 256, device="cuda")
+idx = torch.randint(0, 8, (300, 2), device="cuda", dtype=torch.int32)
+i = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")
+f = lambda *s: torch.zeros(*s, device="cuda")
+c = lambda *s: torch.zeros(*s, dtype=torch.uint8, device="cuda")
+T = [i(8), i(9), i(600), i(300, 2), c(600, 256), f(2, 600), c(8, 256, 256), f(8, 2, 2), f(600, 256), i(9), f(8), f(1), f(300, 8)]
+w, logits, dloss, ws = torch.randn(8, 256, 256, device="cuda"), torch.randn(300, 8, device="cuda"), torch.ones(1, device="cuda"), c(1 << 20)
+def run():
+    bq.moe_expert_plan(idx, 8, *T[:4])
+    bq.moe_fp8_quantize(x, T[4], T[5], rows=T[2])
+    bq.moe_fp8_quantize_weight(w, T[6], T[7])
+    bq.moe_fp8_grouped_matmul(T[4], T[5], T[6], T[7], T[1], T[8])
+    bq.moe_balance_loss(logits, idx, T[9], T[10], T[11], ws)
+    bq.moe_balance_loss_backward(logits, T[9], 2, dloss, T[12])
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    run()
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in T]
+for t in T:
+    t.zero_()
+run()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, T)) and float(T[8].abs().sum()) > 0
+print("same")
+"""
+
+
+def test_first_calls_may_be_captured():
+    """A process whose first calls of every operator are inside a capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
