@@ -19,11 +19,11 @@
 // the next block is multiplied: one FMA per 128 multiply-adds.  That split
 // also keeps the tensor core's accumulation short.
 //
-//   warps 0 .. E-1  epilogue: a thread owns one weight row (tensor-memory lane)
-//                   and the tile's columns (two warpgroups: half of them each)
-//   warp E          TMA producer of weight and token rows (128-byte swizzle)
-//   warp E+1        MMA issuer (one elected thread)
-//   warp E+2        scales: a_scale * b_scale of each block into a small ring
+//   warps 0-3  epilogue: a thread owns one weight row (tensor-memory lane) and the
+//              tile's columns
+//   warp 4     TMA producer of weight and token rows (128-byte swizzle)
+//   warp 5     MMA issuer (one elected thread)
+//   warp 6     scales: a_scale * b_scale of each block into a small ring
 //
 // Few tiles (decode): the K blocks of a tile are split over the CTAs of a
 // cluster, whose partial sums meet through distributed shared memory in rank
@@ -36,24 +36,23 @@ namespace {
 
 using namespace fp8;
 
-template <int BN_, int STAGES_, int BUFS_, int EPI_, int BOX_, int MIN_CTAS_>
+constexpr int kEpiWarps = 4, kThreads = 32 * (kEpiWarps + 3);
+constexpr int kBox = 16;   // token rows of one TMA box
+constexpr int kBufs = 4;   // tensor-memory buffers
+constexpr int kScales = 8;  // ring of scale rows
+
+template <int BN_, int STAGES_>
 struct Config {
-    static constexpr int BN = BN_;          // widest token tile
-    static constexpr int STAGES = STAGES_;  // operand ring
-    static constexpr int BUFS = BUFS_;      // tensor-memory buffers of BN columns
-    static constexpr int EPI = EPI_;        // epilogue warps (4 or 8)
-    static constexpr int BOX = BOX_;        // token rows of one TMA box
-    static constexpr int MIN_CTAS = MIN_CTAS_;
-    static constexpr int COLS = BN * 4 / EPI;  // columns of an epilogue thread
-    static constexpr int THREADS = 32 * (EPI + 3);
-    static constexpr int SCALES = 8;           // ring of scale rows
+    static constexpr int BN = BN_;          // widest token tile, columns of an epilogue thread
+    static constexpr int STAGES = STAGES_;  // operand ring; two CTAs share an SM
     static constexpr int STAGE_BYTES = kABytes + BN * 128;
     static constexpr int TABLE = 2 * (kMaxExperts + 1) * 4;  // group offsets, first tiles
-    static constexpr int SMEM = STAGES * STAGE_BYTES + SCALES * BN * 4 + TABLE + 1024;
-    static_assert(STAGES * STAGE_BYTES >= kWeightRows * BN * 4 || MIN_CTAS == 1, "partial tile fits the operand ring");
+    static constexpr int SMEM = STAGES * STAGE_BYTES + kScales * BN * 4 + TABLE + 1024;
+    static_assert(STAGES * STAGE_BYTES >= kWeightRows * BN * 4, "partial tile fits the operand ring");
+    static_assert(2 * (SMEM + 2048) <= 228 * 1024, "two CTAs an SM");
 };
-typedef Config<64, 4, 4, 4, 16, 2> Narrow;
-typedef Config<16, 5, 4, 4, 16, 2> Token;  // at most 16 rows: a deeper ring of smaller stages
+typedef Config<64, 4> Narrow;
+typedef Config<16, 5> Token;  // at most 16 rows: a deeper ring of smaller stages
 
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                        uint32_t accumulate)
@@ -99,47 +98,47 @@ __device__ __forceinline__ void fma_pair(float2 &acc, uint32_t v0, uint32_t v1, 
 template <class C, int RANKS, class OUT>
 __device__ __forceinline__ void add_partials(uint32_t own, int rank, int cols, OUT *out, int64_t ld)
 {
-    constexpr int STEP = RANKS * (C::EPI / 4), N = 32 / RANKS;
+    constexpr int N = 32 / RANKS;
 #pragma unroll 1
-    for (int c0 = rank * (C::EPI / 4) + (threadIdx.x >> 7); c0 < cols; c0 += N * STEP) {
+    for (int c0 = rank; c0 < cols; c0 += N * RANKS) {
         float p[N][RANKS];
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
             for (int r = 0; r < RANKS; ++r) {
                 p[i][r] = 0.f;
-                if (c0 + i * STEP < cols) p[i][r] = cluster_ld_f32(cluster_map(own + (c0 + i * STEP) * kWeightRows * 4, r));
+                if (c0 + i * RANKS < cols) p[i][r] = cluster_ld_f32(cluster_map(own + (c0 + i * RANKS) * kWeightRows * 4, r));
             }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             float v = p[i][0];
 #pragma unroll
             for (int r = 1; r < RANKS; ++r) v += p[i][r];
-            if (c0 + i * STEP < cols) out[(int64_t)(c0 + i * STEP) * ld] = OUT(v);
+            if (c0 + i * RANKS < cols) out[(int64_t)(c0 + i * RANKS) * ld] = OUT(v);
         }
     }
 }
 
 template <class C, class OUT>
-__global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
+__global__ void __launch_bounds__(kThreads, 2)
     fp8_product_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                        const ProductArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full[C::STAGES], empty[C::STAGES], acc_full[C::BUFS], acc_empty[C::BUFS],
-        sc_full[C::SCALES], sc_empty[C::SCALES], drain_bar;
+    __shared__ __align__(8) uint64_t full[C::STAGES], empty[C::STAGES], acc_full[kBufs], acc_empty[kBufs],
+        sc_full[kScales], sc_empty[kScales], drain_bar;
     __shared__ uint32_t tmem_base;
-    __shared__ int warp_tiles[C::THREADS / 32];
+    __shared__ int warp_tiles[kThreads / 32];
     __shared__ volatile int abort_flag;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *scale_ring = reinterpret_cast<float *>(smem + C::STAGES * C::STAGE_BYTES);
-    int *offset = reinterpret_cast<int *>(scale_ring + C::SCALES * C::BN);
+    int *offset = reinterpret_cast<int *>(scale_ring + kScales * C::BN);
     int *first_tile = offset + kMaxExperts + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned rank = cluster_rank(), ranks = cluster_size();
 
-    if (warp == C::EPI + 1) {
-        tmem_alloc(&tmem_base, C::BUFS * C::BN);
+    if (warp == kEpiWarps + 1) {
+        tmem_alloc(&tmem_base, kBufs * C::BN);
         tmem_relinquish();
     }
     if (threadIdx.x == 0) {
@@ -147,19 +146,19 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int s = 0; s < C::BUFS; ++s) {
+        for (int s = 0; s < kBufs; ++s) {
             mbar_init(&acc_full[s], 1);
-            mbar_init(&acc_empty[s], C::EPI);
+            mbar_init(&acc_empty[s], kEpiWarps);
         }
-        for (int s = 0; s < C::SCALES; ++s) {
+        for (int s = 0; s < kScales; ++s) {
             mbar_init(&sc_full[s], 1);
-            mbar_init(&sc_empty[s], C::EPI);
+            mbar_init(&sc_empty[s], kEpiWarps);
         }
         mbar_init(&drain_bar, 1);
         abort_flag = 0;
         fence_mbar_init();
     }
-    build_groups<C::THREADS>(a, C::BN, offset, first_tile, warp_tiles);
+    build_groups<kThreads>(a, C::BN, offset, first_tile, warp_tiles);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -173,34 +172,34 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
     // One tile of each role; after a wait that ran out a warp skips its work (and the others'
     // waits run out) but still meets the cluster's barriers.
     Ring<C::STAGES> ring;  // this warp's positions
-    Ring<C::BUFS> buf;
-    Ring<C::SCALES> scale;
+    Ring<kBufs> buf;
+    Ring<kScales> scale;
     bool go = true;
     TileWalk walk(worker, workers, a.n_tiles);
     for (int id = worker; id < n_work; id += workers, walk.next()) {
         const Tile t = walk.tile(a.groups, first_tile, offset);
         const int ncols = (max(t.rows, 1) + 15) & ~15;
-        float2 acc[C::COLS / 2];
+        float2 acc[C::BN / 2];
         // (the issuing warps run converged and one lane issues: in a branch of one lane descriptors
         // do not count as uniform, and each instruction costs a sequence of moves)
-        if (warp == C::EPI) {  // ---- TMA producer
-            const int boxes = (ncols + C::BOX - 1) / C::BOX;
+        if (warp == kEpiWarps) {  // ---- TMA producer
+            const int boxes = (ncols + kBox - 1) / kBox;
             for (int kb = kb0; kb < kb1 && go; ++kb) {
                 go = __all_sync(0xffffffffu, bar_wait(smem_u32(empty) + 8 * ring.slot, ring.phase ^ 1));
                 if (!go) break;
                 if (elect_one()) {
                     uint8_t *w_s = smem + ring.slot * C::STAGE_BYTES, *x_s = w_s + kABytes;
                     uint64_t *bar = &full[ring.slot];
-                    mbar_arrive_expect_tx(bar, kABytes + boxes * C::BOX * 128);
+                    mbar_arrive_expect_tx(bar, kABytes + boxes * kBox * 128);
                     tma_load_3d(w_s, &map_w, bar, kb * 128, t.n_tile * kWeightRows, t.group);
                     for (int b = 0; b < boxes; ++b)
-                        tma_load_2d(x_s + b * C::BOX * 128, &map_x, bar, kb * 128, t.row0 + b * C::BOX);
+                        tma_load_2d(x_s + b * kBox * 128, &map_x, bar, kb * 128, t.row0 + b * kBox);
                 }
                 __syncwarp();
                 ++issued;
                 ring.next();
             }
-        } else if (warp == C::EPI + 1) {  // ---- MMA issuer
+        } else if (warp == kEpiWarps + 1) {  // ---- MMA issuer
             const uint32_t idesc = idesc_e4m3(kWeightRows, ncols);
             for (int kb = kb0; kb < kb1 && go; ++kb) {
                 const bool ok = bar_wait(smem_u32(full) + 8 * ring.slot, ring.phase) &&
@@ -220,7 +219,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
                 ring.next();
                 buf.next();
             }
-        } else if (warp == C::EPI + 2) {  // ---- scales
+        } else if (warp == kEpiWarps + 2) {  // ---- scales
             constexpr int PER = (C::BN + 31) / 32;  // columns of a lane
             constexpr int AHEAD = PER == 1 ? 8 : 4;  // blocks of loads in flight
             const float *bs = a.b_scale + ((int64_t)t.group * a.n_tiles + t.n_tile) * a.kblocks;
@@ -250,9 +249,8 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
                 }
             }
         } else {  // ---- epilogue warps
-            const int part = warp >> 2, c0 = part * C::COLS;
 #pragma unroll
-            for (int i = 0; i < C::COLS / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+            for (int i = 0; i < C::BN / 2; ++i) acc[i] = make_float2(0.f, 0.f);
             for (int kb = kb0; kb < kb1 && go; ++kb) {
                 const int d = buf.slot, s = scale.slot;
                 const uint32_t sc_at = smem_u32(sc_full) + 8 * s, acc_at = smem_u32(acc_full) + 8 * d;
@@ -265,11 +263,11 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
                 buf.next();
                 scale.next();
                 tc_fence_after_sync();
-                const uint32_t td = tmem + d * C::BN + c0 + ((uint32_t)((warp & 3) * 32) << 16);
-                const float *sc = scale_ring + s * C::BN + c0;
+                const uint32_t td = tmem + d * C::BN + ((uint32_t)(warp * 32) << 16);
+                const float *sc = scale_ring + s * C::BN;
 #pragma unroll
-                for (int c = 0; c < C::COLS; c += 16) {
-                    if (c0 + c < ncols) {
+                for (int c = 0; c < C::BN; c += 16) {
+                    if (c < ncols) {
                         uint32_t v[16];
                         tmem_request16(td + c, v);
                         tmem_wait16(v);
@@ -295,21 +293,21 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
             // partial sums of the cluster's CTAs, added in rank order; the operand ring is
             // idle here (its last block has been multiplied) and holds this CTA's partial
             float *partial = reinterpret_cast<float *>(smem);  // [column][weight row]
-            if (warp < C::EPI) {
-                const int c0 = (warp >> 2) * C::COLS, m = (warp & 3) * 32 + lane;
+            if (warp < kEpiWarps) {
+                const int m = threadIdx.x;
 #pragma unroll
-                for (int i = 0; i < C::COLS / 2; ++i) {
-                    if (c0 + 2 * i < ncols) {
-                        partial[(c0 + 2 * i) * kWeightRows + m] = acc[i].x;
-                        partial[(c0 + 2 * i + 1) * kWeightRows + m] = acc[i].y;
+                for (int i = 0; i < C::BN / 2; ++i) {
+                    if (2 * i < ncols) {
+                        partial[2 * i * kWeightRows + m] = acc[i].x;
+                        partial[(2 * i + 1) * kWeightRows + m] = acc[i].y;
                     }
                 }
             }
             cluster_sync();
-            if (warp < C::EPI && !abort_flag) {
-                const int n = t.n_tile * kWeightRows + (threadIdx.x & 127);
+            if (warp < kEpiWarps && !abort_flag) {
+                const int n = t.n_tile * kWeightRows + (int)threadIdx.x;
                 OUT *out = static_cast<OUT *>(a.out) + (int64_t)t.row0 * a.ld_out + n;
-                const uint32_t own = smem_u32(partial + (threadIdx.x & 127));
+                const uint32_t own = smem_u32(partial + threadIdx.x);
                 const int cols = n < a.n ? t.rows : 0;
                 if (ranks == 2) add_partials<C, 2>(own, (int)rank, cols, out, a.ld_out);
                 else if (ranks == 4) add_partials<C, 4>(own, (int)rank, cols, out, a.ld_out);
@@ -317,28 +315,28 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
             }
             fence_proxy_async_smem();  // the ring is written by TMA again
             cluster_sync();
-        } else if (warp < C::EPI && !abort_flag) {
-            const int c0 = (warp >> 2) * C::COLS, n = t.n_tile * kWeightRows + (warp & 3) * 32 + lane;
+        } else if (warp < kEpiWarps && !abort_flag) {
+            const int n = t.n_tile * kWeightRows + (int)threadIdx.x;
             if (n < a.n) {
-                OUT *out = static_cast<OUT *>(a.out) + (int64_t)(t.row0 + c0) * a.ld_out + n;
+                OUT *out = static_cast<OUT *>(a.out) + (int64_t)t.row0 * a.ld_out + n;
 #pragma unroll
-                for (int i = 0; i < C::COLS / 2; ++i) {
-                    if (c0 + 2 * i < t.rows) out[(int64_t)(2 * i) * a.ld_out] = OUT(acc[i].x);
-                    if (c0 + 2 * i + 1 < t.rows) out[(int64_t)(2 * i + 1) * a.ld_out] = OUT(acc[i].y);
+                for (int i = 0; i < C::BN / 2; ++i) {
+                    if (2 * i < t.rows) out[(int64_t)(2 * i) * a.ld_out] = OUT(acc[i].x);
+                    if (2 * i + 1 < t.rows) out[(int64_t)(2 * i + 1) * a.ld_out] = OUT(acc[i].y);
                 }
             }
         }
     }
     // after a timed-out wait: let copies and MMAs in flight land before memory is released
     if (abort_flag) {
-        if (warp == C::EPI && lane == 0) drain_ring(full, C::STAGES, issued);
-        if (warp == C::EPI + 1 && elect_one()) drain_mma(&drain_bar);
+        if (warp == kEpiWarps && lane == 0) drain_ring(full, C::STAGES, issued);
+        if (warp == kEpiWarps + 1 && elect_one()) drain_mma(&drain_bar);
         if (threadIdx.x == 0 && a.status) atomicExch(a.status, (int)MOE_ERR_TIMEOUT);
     }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (warp == C::EPI + 1) tmem_dealloc(tmem, C::BUFS * C::BN);
+    if (warp == kEpiWarps + 1) tmem_dealloc(tmem, kBufs * C::BN);
 }
 
 template <class C>
@@ -355,11 +353,11 @@ moe_status run_product(const Operands &o, const ProductArgs &a, moe_dtype out_dt
 {
     CUtensorMap mw, mx;
     if (!code_map(&mw, o.b, o.k, a.n, o.ld_b, a.groups, o.stride_b, kWeightRows)) return MOE_ERR_CUDA;
-    if (!code_map(&mx, o.a, o.k, a.rows, o.ld_a, 0, 0, C::BOX)) return MOE_ERR_CUDA;
+    if (!code_map(&mx, o.a, o.k, a.rows, o.ld_a, 0, 0, kBox)) return MOE_ERR_CUDA;
     const dim3 grid(workers * ranks);
-    return launched(out_dtype == MOE_DT_BF16 ? launch(fp8_product_kernel<C, __nv_bfloat16>, grid, C::THREADS, C::SMEM, s,
+    return launched(out_dtype == MOE_DT_BF16 ? launch(fp8_product_kernel<C, __nv_bfloat16>, grid, kThreads, C::SMEM, s,
                                                       ranks, false, mw, mx, a)
-                                             : launch(fp8_product_kernel<C, float>, grid, C::THREADS, C::SMEM, s, ranks,
+                                             : launch(fp8_product_kernel<C, float>, grid, kThreads, C::SMEM, s, ranks,
                                                       false, mw, mx, a));
 }
 
