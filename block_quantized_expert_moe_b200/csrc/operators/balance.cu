@@ -245,10 +245,10 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_forward_kernel(const B
     __shared__ int32_t cta_valid;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const T *logits = static_cast<const T *>(a.logits);
-    if (!CLUSTER) dependents_launch();  // the second kernel may wait on the SMs
     for (int e = threadIdx.x; e < a.E; e += kBalThreads) hist[e] = 0;
     if (threadIdx.x == 0) cta_valid = 0;
     __syncthreads();
+    follow_previous();
 
     float acc[NV];
 #pragma unroll
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_forward_kernel(const B
 
 __global__ void __launch_bounds__(kBalThreads, 1) balance_reduce_kernel(const BalanceArgs a)
 {
-    dependents_wait();
+    follow_previous();
     balance_reduce<false>(a, nullptr, nullptr, nullptr);
 }
 
@@ -328,6 +328,7 @@ __global__ void __launch_bounds__(kBwdThreads)
                             T *__restrict__ dlogits)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    follow_previous();
     const double n = (double)max(__ldg(counts + E), 1);
     const float to_share = (float)((double)E / ((double)k * n));
     const float scale = __ldg(dloss) / (float)n;
@@ -485,9 +486,9 @@ extern "C" moe_status moe_balance_loss(const void *logits, moe_dtype dtype, cons
     ForwardKernel f = dtype == MOE_DT_BF16 ? forward_pick<__nv_bfloat16, 8>(n_experts, wide, cluster)
                                            : forward_pick<float, 4>(n_experts, wide, cluster);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch(f, dim3(a.ctas), kBalThreads, balance_smem(n_experts), s, cluster ? a.ctas : 1, false, a);
+    cudaError_t e = launch(f, dim3(a.ctas), kBalThreads, balance_smem(n_experts), s, cluster ? a.ctas : 1, a);
     if (e == cudaSuccess && !cluster)
-        e = launch(balance_reduce_kernel, dim3(kBalCluster), kBalThreads, 0, s, kBalCluster, true, a);
+        e = launch(balance_reduce_kernel, dim3(kBalCluster), kBalThreads, 0, s, kBalCluster, a);
     return launched(e);
 }
 
@@ -507,13 +508,13 @@ extern "C" moe_status moe_balance_loss_backward(const void *logits, moe_dtype dt
     const bool wide = wide_rows(logits, dlogits, dtype, n_experts);
     const int grid = std::min(ceil_div(n_tokens, kBwdWarps), sms * 4);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (dtype == MOE_DT_BF16)
-        backward_pick<__nv_bfloat16, 8>(n_experts, wide)<<<grid, kBwdThreads, 0, s>>>(
-            static_cast<const __nv_bfloat16 *>(logits), counts, valid, dloss, n_tokens, n_experts, top_k,
-            static_cast<__nv_bfloat16 *>(dlogits));
-    else
-        backward_pick<float, 4>(n_experts, wide)<<<grid, kBwdThreads, 0, s>>>(
-            static_cast<const float *>(logits), counts, valid, dloss, n_tokens, n_experts, top_k,
-            static_cast<float *>(dlogits));
-    return launched(cudaGetLastError());
+    const cudaError_t e =
+        dtype == MOE_DT_BF16
+            ? launch(backward_pick<__nv_bfloat16, 8>(n_experts, wide), dim3(grid), kBwdThreads, 0, s, 1,
+                     static_cast<const __nv_bfloat16 *>(logits), counts, valid, dloss, n_tokens, n_experts, top_k,
+                     static_cast<__nv_bfloat16 *>(dlogits))
+            : launch(backward_pick<float, 4>(n_experts, wide), dim3(grid), kBwdThreads, 0, s, 1,
+                     static_cast<const float *>(logits), counts, valid, dloss, n_tokens, n_experts, top_k,
+                     static_cast<float *>(dlogits));
+    return launched(e);
 }

@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
         for (int i = threadIdx.x; i < words; i += kPlanThreads) hist[i] = 0;
     }
     __syncthreads();
+    follow_previous();
 
     const int n_warps = warps * (int)ctas;
     const int chunk = (int)((((int64_t)P + n_warps - 1) / n_warps + 31) & ~31ll);
@@ -248,6 +249,6 @@ extern "C" moe_status moe_expert_plan(const int32_t *idx, int n_tokens, int top_
         ctas = g_plan_cluster[dev];
     }
     return launched(launch(expert_plan_kernel, dim3(ctas), kPlanThreads, plan_smem(n_experts, warps),
-                           static_cast<cudaStream_t>(stream), ctas, false, idx, (int)pairs, top_k, n_experts, bits, warps,
+                           static_cast<cudaStream_t>(stream), ctas, idx, (int)pairs, top_k, n_experts, bits, warps,
                            counts, offsets, rows, slots));
 }

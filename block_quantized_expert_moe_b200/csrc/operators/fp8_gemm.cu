@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         abort_flag = 0;
         fence_mbar_init();
     }
+    follow_previous();
     build_groups<kThreads>(a, C::BN, offset, first_tile, warp_tiles);
     tc_fence_before_sync();
     __syncthreads();
@@ -356,9 +357,9 @@ moe_status run_product(const Operands &o, const ProductArgs &a, moe_dtype out_dt
     if (!code_map(&mx, o.a, o.k, a.rows, o.ld_a, 0, 0, kBox)) return MOE_ERR_CUDA;
     const dim3 grid(workers * ranks);
     return launched(out_dtype == MOE_DT_BF16 ? launch(fp8_product_kernel<C, __nv_bfloat16>, grid, kThreads, C::SMEM, s,
-                                                      ranks, false, mw, mx, a)
+                                                      ranks, mw, mx, a)
                                              : launch(fp8_product_kernel<C, float>, grid, kThreads, C::SMEM, s, ranks,
-                                                      false, mw, mx, a));
+                                                      mw, mx, a));
 }
 
 PerDevice g_product;

@@ -255,6 +255,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         abort_flag = 0;
         fence_mbar_init();
     }
+    follow_previous();
     build_groups<kPairThreads>(a, kPairTokens, offset, first_tile, warp_tiles);
     tc_fence_before_sync();
     __syncthreads();
@@ -459,8 +460,8 @@ template <class OUT>
 cudaError_t pair_launch(const CUtensorMap &mw, const CUtensorMap &mx, const CUtensorMap &my, const ProductArgs &a,
                         bool wide, int pairs, cudaStream_t s)
 {
-    return wide ? launch(fp8_pair_kernel<OUT, true>, dim3(2 * pairs), kPairThreads, kPairSmem, s, 2, false, mw, mx, my, a)
-                : launch(fp8_pair_kernel<OUT, false>, dim3(2 * pairs), kPairThreads, kPairSmem, s, 2, false, mw, mx, my, a);
+    return wide ? launch(fp8_pair_kernel<OUT, true>, dim3(2 * pairs), kPairThreads, kPairSmem, s, 2, mw, mx, my, a)
+                : launch(fp8_pair_kernel<OUT, false>, dim3(2 * pairs), kPairThreads, kPairSmem, s, 2, mw, mx, my, a);
 }
 
 }  // namespace

@@ -179,6 +179,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const Quan
 {
     const int half = threadIdx.x >> 4, lane = threadIdx.x & 15;
     const int row = blockIdx.x * kQuantRows + (half & (kQuantRows - 1));
+    follow_previous();
     const T *x = nullptr;
     if (row < a.rows) {
         const int src = a.index ? __ldg(a.index + row) : row;
@@ -242,6 +243,7 @@ __global__ void __launch_bounds__(kQuantThreads)
     const int c0 = kb * kScaleBlock + (threadIdx.x & 15) * 8;
     const int r0 = nb * kScaleBlock + (threadIdx.x >> 4);
     const T *src = w + (int64_t)g * group_stride;
+    follow_previous();
     float v[8][8];
     float m = 0.f;
 #pragma unroll
@@ -329,8 +331,7 @@ extern "C" moe_status moe_fp8_quantize(const void *x, moe_dtype x_dtype, int64_t
     const int row_ctas = ceil_div(n_rows, kQuantRows);
     // few rows: a CTA per turn of blocks; many: a CTA walks its rows' blocks
     const int by = std::max(1, std::min(ceil_div(a.blocks, kQuantTurn), 1184 / row_ctas));
-    f<<<dim3(row_ctas, by), kQuantThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    return launched(cudaGetLastError());
+    return launched(launch(f, dim3(row_ctas, by), kQuantThreads, 0, static_cast<cudaStream_t>(stream), 1, a));
 }
 
 extern "C" moe_status moe_fp8_quantize_weight(const void *w, moe_dtype w_dtype, int64_t ld_w, int64_t group_stride_w,
@@ -351,12 +352,10 @@ extern "C" moe_status moe_fp8_quantize_weight(const void *w, moe_dtype w_dtype, 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (w_dtype == MOE_DT_BF16) {
         auto f = wide ? quantize_weight_kernel<__nv_bfloat16, true> : quantize_weight_kernel<__nv_bfloat16, false>;
-        f<<<grid, kQuantThreads, 0, s>>>(static_cast<const __nv_bfloat16 *>(w), ld_w, group_stride_w, n, cols, codes,
-                                         ld_codes, group_stride_codes, scales);
-    } else {
-        auto f = wide ? quantize_weight_kernel<float, true> : quantize_weight_kernel<float, false>;
-        f<<<grid, kQuantThreads, 0, s>>>(static_cast<const float *>(w), ld_w, group_stride_w, n, cols, codes, ld_codes,
-                                         group_stride_codes, scales);
+        return launched(launch(f, grid, kQuantThreads, 0, s, 1, static_cast<const __nv_bfloat16 *>(w), ld_w,
+                               group_stride_w, n, cols, codes, ld_codes, group_stride_codes, scales));
     }
-    return launched(cudaGetLastError());
+    auto f = wide ? quantize_weight_kernel<float, true> : quantize_weight_kernel<float, false>;
+    return launched(launch(f, grid, kQuantThreads, 0, s, 1, static_cast<const float *>(w), ld_w, group_stride_w, n, cols,
+                           codes, ld_codes, group_stride_codes, scales));
 }

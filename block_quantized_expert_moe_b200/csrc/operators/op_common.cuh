@@ -45,9 +45,11 @@ struct PerDevice {
 
 inline moe_status launched(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
+// Every operator is launched as a programmatic dependent of what precedes it on the stream:
+// its blocks may be set up while that finishes, and each kernel begins with
+// follow_previous(), before it touches global memory.
 template <class K, class... A>
-inline cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, int cluster, bool dependent,
-                          A... args)
+inline cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, int cluster, A... args)
 {
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg{};
@@ -63,11 +65,9 @@ inline cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, cudaStr
         attr[cfg.numAttrs].val.clusterDim.z = 1;
         ++cfg.numAttrs;
     }
-    if (dependent) {
-        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
-        ++cfg.numAttrs;
-    }
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -113,8 +113,13 @@ __device__ __forceinline__ float cluster_ld_f32(uint32_t addr)
     return v;
 }
 
-__device__ __forceinline__ void dependents_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Waits until everything before this kernel on the stream has finished and its memory is
+// visible, then lets the next kernel's blocks be set up (in this order: a follower that
+// reads weights before its own wait must not overtake what precedes this kernel).
+__device__ __forceinline__ void follow_previous()
+{
+    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
 
 }  // namespace op
 }  // namespace moe

@@ -669,3 +669,53 @@ def test_first_calls_may_be_captured():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+def test_operators_between_layer_forwards():
+    """Operators and whole-layer forwards one after another on one stream, nothing waited for (each is set up
+    while the one before it finishes), eager and captured: the results of the calls run one by one."""
+    import synth
+    from harness import router_to_device, to_device
+    m = bq()
+    wl = synth.WORKLOADS["tiny_q8"]
+    li = synth.layer_inputs(wl, 0)
+    packs, xs, outs = [], [], []
+    for T in (1, 4):  # the single-token kernel and the one-launch tail
+        packs.append(m.pack_layer(li, max_tokens=T))
+        xs.append(to_device(synth.tokens(wl, li.router, 0, 0, T)))
+        outs.append(torch.zeros(T, wl.hidden, device="cuda"))
+    wr = router_to_device(li.router)
+    layer = Layer(40, 16, 4, 256, 128, 9)
+    layer.logits.copy_(layer.x.float() @ layer.router.float().t())
+
+    def forward(i):
+        m.moe_layer_forward(xs[i], wr, packs[i], m.MOE_FMT_FROM_PACK, wl.top_k, outs[i])
+
+    def sequence(wait):
+        for i in (0, 1, 0, 1):
+            layer.run()
+            wait()
+            forward(i)
+            wait()
+
+    results = lambda: [t.clone() for t in (*outs, layer.y, layer.dlogits, layer.loss, layer.slots)]
+    sequence(torch.cuda.synchronize)
+    want = results()
+    for _ in range(3):
+        for t in (*outs, layer.y, layer.dlogits, layer.loss):
+            t.zero_()
+        sequence(lambda: None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(results(), want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        sequence(lambda: None)
+    for _ in range(3):
+        for t in (*outs, layer.y, layer.dlogits, layer.loss):
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(results(), want))
+    for p in packs:
+        assert m.moe_get_device_error(p) == m.MOE_OK
+        p.free()
