@@ -35,28 +35,27 @@ constexpr int kBalCluster = 8;      // CTAs of the cluster that adds the column 
 constexpr int kBalMaxCtas = 148;    // CTAs with partial sums in the workspace
 constexpr int kBalOneLaunch = 128;  // tokens of one cluster, a row a warp (512 tokens, 512 experts: 9.9 us; two launches 7.4)
 
-// A lane's values of a row: NV of them, V consecutive at a time (16 bytes, or
-// one where rows are not 16-byte aligned); value (i, j) is column
-// (i * 32 + lane) * V + j.
+// V consecutive values of a row: 16 bytes, or one where rows are not 16-byte aligned.
 template <class T, int V>
-struct RowVec;
+struct Raw;
 template <>
-struct RowVec<float, 4> {
-    static __device__ __forceinline__ void load(const float *p, float (&v)[4])
-    {
-        const float4 r = __ldg(reinterpret_cast<const float4 *>(p));
-        v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w;
-    }
-    static __device__ __forceinline__ void store(float *p, const float (&v)[4])
+struct Raw<float, 4> {
+    float4 r;
+    __device__ __forceinline__ void load(const float *p) { r = __ldg(reinterpret_cast<const float4 *>(p)); }
+    __device__ __forceinline__ void fill() { r = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
+    __device__ __forceinline__ void values(float *v) const { v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w; }
+    static __device__ __forceinline__ void store(float *p, const float *v)
     {
         *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
     }
 };
 template <>
-struct RowVec<__nv_bfloat16, 8> {
-    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float (&v)[8])
+struct Raw<__nv_bfloat16, 8> {
+    uint4 r;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { r = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void fill() { r = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
+    __device__ __forceinline__ void values(float *v) const
     {
-        const uint4 r = __ldg(reinterpret_cast<const uint4 *>(p));
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -64,7 +63,7 @@ struct RowVec<__nv_bfloat16, 8> {
             v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
     }
-    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[8])
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float *v)
     {
         uint32_t w[4];
 #pragma unroll
@@ -76,30 +75,42 @@ struct RowVec<__nv_bfloat16, 8> {
     }
 };
 template <>
-struct RowVec<float, 1> {
-    static __device__ __forceinline__ void load(const float *p, float (&v)[1]) { v[0] = __ldg(p); }
-    static __device__ __forceinline__ void store(float *p, const float (&v)[1]) { *p = v[0]; }
+struct Raw<float, 1> {
+    float r;
+    __device__ __forceinline__ void load(const float *p) { r = __ldg(p); }
+    __device__ __forceinline__ void fill() { r = -INFINITY; }
+    __device__ __forceinline__ void values(float *v) const { v[0] = r; }
+    static __device__ __forceinline__ void store(float *p, const float *v) { *p = v[0]; }
 };
 template <>
-struct RowVec<__nv_bfloat16, 1> {
-    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float (&v)[1]) { v[0] = __bfloat162float(*p); }
-    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[1]) { *p = __float2bfloat16_rn(v[0]); }
+struct Raw<__nv_bfloat16, 1> {
+    __nv_bfloat16 r;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { r = *p; }
+    __device__ __forceinline__ void fill() { r = __ushort_as_bfloat16(0xff80); }
+    __device__ __forceinline__ void values(float *v) const { v[0] = __bfloat162float(r); }
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float *v) { *p = __float2bfloat16_rn(v[0]); }
 };
 
+// A lane's NV values of a row as loaded (bf16 in half the registers): value (i, j) is column
+// (i * 32 + lane) * V + j, -inf behind the row's end.
 template <class T, int NV, int V>
-__device__ __forceinline__ void load_row(const T *row, int E, int lane, float (&v)[NV])
-{
+struct Row {
+    Raw<T, V> raw[NV / V];
+    __device__ __forceinline__ void load(const T *row, int E, int lane)
+    {
 #pragma unroll
-    for (int i = 0; i < NV / V; ++i) {
-        const int c = (i * 32 + lane) * V;
-        float u[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) u[j] = -INFINITY;
-        if (c < E) RowVec<T, V>::load(row + c, u);  // V > 1 only where E is a multiple of V
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[i * V + j] = u[j];
+        for (int i = 0; i < NV / V; ++i) {
+            const int c = (i * 32 + lane) * V;
+            raw[i].fill();
+            if (c < E) raw[i].load(row + c);  // V > 1 only where E is a multiple of V
+        }
     }
-}
+    __device__ __forceinline__ void values(float (&v)[NV]) const
+    {
+#pragma unroll
+        for (int i = 0; i < NV / V; ++i) raw[i].values(v + i * V);
+    }
+};
 
 // v becomes the row's probabilities.  A row of only -inf has none (all zero); a
 // NaN or +inf makes the whole row NaN, as the definition does.
@@ -257,19 +268,18 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_forward_kernel(const B
     const int step = gridDim.x * kBalWarps;
     int t = blockIdx.x * kBalWarps + warp;
     // the next row's logits, mask and choices are in flight while this one is summed
-    float next[NV];
+    Row<T, NV, V> next;
     int next_choice = -1;
     bool next_valid = true;
     const auto fetch = [&](int row) {
-        load_row<T, NV, V>(logits + (size_t)row * a.E, a.E, lane, next);
+        next.load(logits + (size_t)row * a.E, a.E, lane);
         next_valid = !a.valid || __ldg(a.valid + row);
         next_choice = lane < a.k ? __ldg(a.idx + (size_t)row * a.k + lane) : -1;
     };
     if (t < a.T) fetch(t);
     for (; t < a.T; t += step) {
         float v[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) v[i] = next[i];
+        next.values(v);
         const int choice = next_choice;
         const bool counted = next_valid;
         if (t + step < a.T) fetch(t + step);
@@ -343,7 +353,9 @@ __global__ void __launch_bounds__(kBwdThreads)
     // (a row ahead in registers costs more warps than it hides: 30.6 against 46.4 us at 65,536 x 512)
     for (int t = blockIdx.x * kBwdWarps + warp; t < tokens; t += gridDim.x * kBwdWarps) {
         float v[NV];
-        load_row<T, NV, V>(logits + (size_t)t * E, E, lane, v);  // not held up by the mask
+        Row<T, NV, V> row;
+        row.load(logits + (size_t)t * E, E, lane);  // not held up by the mask
+        row.values(v);
         if (!valid || __ldg(valid + t)) {
             row_softmax<NV>(v);
             float dot = 0.f;
@@ -360,10 +372,7 @@ __global__ void __launch_bounds__(kBwdThreads)
 #pragma unroll
         for (int i = 0; i < NV / V; ++i) {
             const int c = (i * 32 + lane) * V;
-            float u[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) u[j] = v[i * V + j];
-            if (c < E) RowVec<T, V>::store(dlogits + (size_t)t * E + c, u);
+            if (c < E) Raw<T, V>::store(dlogits + (size_t)t * E + c, v + i * V);
         }
     }
 }
