@@ -377,7 +377,7 @@ moe_status product(const uint8_t *a, int64_t ld_a, const float *a_scale, int64_t
                    int k, void *out, moe_dtype out_dtype, int64_t ld_out, int32_t *status, void *stream)
 {
     if (out_dtype != MOE_DT_F32 && out_dtype != MOE_DT_BF16) return MOE_ERR_INVALID_ARG;
-    if (rows < 0 || n < 1 || n > (1 << 20) || k < 1 || k > (1 << 20) || groups < 1 || groups > kMaxExperts)
+    if (rows < 0 || rows > kMaxRows || n < 1 || n > (1 << 20) || k < 1 || k > (1 << 20) || groups < 1 || groups > kMaxExperts)
         return MOE_ERR_INVALID_ARG;
     if (ld_a < k || ld_a % 16 || ld_b < k || ld_b % 16 || stride_b % 16 || ld_out < n || ld_a_scale < rows)
         return MOE_ERR_INVALID_ARG;

@@ -305,7 +305,7 @@ extern "C" moe_status moe_fp8_quantize(const void *x, moe_dtype x_dtype, int64_t
                                        int64_t ld_codes, float *scales, int64_t ld_scales, void *stream)
 {
     if ((x_dtype != MOE_DT_F32 && x_dtype != MOE_DT_BF16) || (swiglu != 0 && swiglu != 1)) return MOE_ERR_INVALID_ARG;
-    if (n_rows < 0 || n_src_rows < 0 || cols < 1 || cols > (1 << 20)) return MOE_ERR_INVALID_ARG;
+    if (n_rows < 0 || n_rows > kMaxRows || n_src_rows < 0 || cols < 1 || cols > (1 << 20)) return MOE_ERR_INVALID_ARG;
     if (!rows && n_src_rows != n_rows) return MOE_ERR_INVALID_ARG;
     if (ld_x < (swiglu ? 2 : 1) * (int64_t)cols || ld_codes < cols || ld_codes % 16 || ld_scales < n_rows)
         return MOE_ERR_INVALID_ARG;

@@ -16,6 +16,7 @@ namespace op {
 constexpr int kMaxExperts = 1024;
 constexpr int kScaleBlock = 128;  // columns that share a scale (weights: 128 x 128)
 constexpr int kMaxDevices = 64;
+constexpr int kMaxRows = 1 << 30;
 
 inline bool aligned(const void *p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 inline int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
@@ -34,8 +35,10 @@ struct PerDevice {
         std::lock_guard<std::mutex> lk(m);
         if (!sms[dev]) {
             int n = 0;
-            if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return MOE_ERR_CUDA;
-            if (prepare() != cudaSuccess) return MOE_ERR_CUDA;
+            if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || prepare() != cudaSuccess) {
+                cudaGetLastError();  // reported here, not by a later call
+                return MOE_ERR_CUDA;
+            }
             sms[dev] = n;
         }
         *out = sms[dev];
@@ -43,7 +46,12 @@ struct PerDevice {
     }
 };
 
-inline moe_status launched(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+inline moe_status launched(cudaError_t e)
+{
+    if (e == cudaSuccess) return MOE_OK;
+    cudaGetLastError();  // reported here, not by a later call
+    return MOE_ERR_CUDA;
+}
 
 // Every operator is launched as a programmatic dependent of what precedes it on the stream:
 // its blocks may be set up while that finishes, and each kernel begins with

@@ -437,8 +437,8 @@ size_t moe_balance_loss_workspace_bytes(int n_tokens, int n_experts);
  *   workspace device, 16-byte aligned, moe_balance_loss_workspace_bytes bytes
  *             (NULL when that is 0); its contents need no initialisation.  Two
  *             calls that may run at the same time need one each.
- * A logit of -inf has probability 0; a token whose logits are all -inf adds
- * nothing to P.  With no token that counts, loss, counts and P are 0.  Sums
+ * 1 <= top_k <= n_experts <= 1024, n_tokens <= 2^30.  A logit of -inf has
+ * probability 0; a token whose logits are all -inf adds nothing to P.  With no token that counts, loss, counts and P are 0.  Sums
  * are fp32 in a fixed order: results are reproducible bit for bit. */
 moe_status moe_balance_loss(const void *logits, moe_dtype dtype, const int32_t *idx, const uint8_t *valid,
                             int n_tokens, int n_experts, int top_k, float *loss, int32_t *counts, float *prob_mean,
@@ -470,7 +470,7 @@ moe_status moe_balance_loss_backward(const void *logits, moe_dtype dtype, const 
  *           written
  *   scales  device [ceil(cols / 128) x n_rows] fp32, one row per block, row
  *           stride ld_scales elements
- * 1 <= cols <= 2^20.  n_rows == 0 enqueues nothing. */
+ * 1 <= cols <= 2^20, n_rows <= 2^30.  n_rows == 0 enqueues nothing. */
 moe_status moe_fp8_quantize(const void *x, moe_dtype x_dtype, int64_t ld_x, const int32_t *rows, int n_src_rows,
                             int n_rows, int cols, int swiglu, uint8_t *codes, int64_t ld_codes, float *scales,
                             int64_t ld_scales, void *stream);
@@ -499,7 +499,7 @@ moe_status moe_fp8_quantize_weight(const void *w, moe_dtype w_dtype, int64_t ld_
  *            bounded wait of the kernel runs out (outputs are then undefined);
  *            otherwise it is not written
  * a and b are 16-byte aligned and their row strides multiples of 16; n and k
- * are any sizes up to 2^20.  rows == 0 enqueues nothing.  The product by the
+ * are any sizes up to 2^20, rows up to 2^30.  rows == 0 enqueues nothing.  The product by the
  * transposed weights (the gradient of a) is the same call on the transposed
  * codes and block scales. */
 moe_status moe_fp8_matmul(const uint8_t *a, int64_t ld_a, const float *a_scale, int64_t ld_a_scale, int rows,

@@ -73,6 +73,15 @@ def test_entry_points_refuse_bad_arguments(name, over):
     assert call(name, **over) == INVALID
 
 
+def test_entry_points_refuse_more_rows_than_they_index():
+    big = (1 << 30) + 1
+    assert call("moe_fp8_quantize", R=big, S=big, lds=big) == INVALID
+    assert call("moe_fp8_matmul", R=big, ldsa=big) == INVALID
+    assert call("moe_fp8_grouped_matmul", R=big, ldsa=big) == INVALID
+    assert call("moe_balance_loss", T=big) == INVALID
+    assert call("moe_balance_loss_backward", T=big) == INVALID
+
+
 def test_empty_batches_enqueue_nothing():
     assert call("moe_balance_loss_backward", T=0, logits=None, dlogits=None, counts=None, dloss=None) == OK
     assert call("moe_fp8_quantize", R=0, S=0, x=None, codes=None, scales=None) == OK
