@@ -133,38 +133,55 @@ __device__ __forceinline__ void load_values(const T *row, int c0, int cols, floa
     }
 }
 
-// the same of a source row, or of its SwiGLU; zeros for no row
+// The lane's eight columns of a block: 8 in a row, or for fp32 rows off 16-byte boundaries every
+// 16th, so that a load is consecutive.  (28,968 gathered rows of 1309: 36.1 us, 41.8 with 8 in a
+// row; for bf16 the codes' byte stores cost more: 60,000 SwiGLU rows of 513 46.4 us, 56.6 with
+// every 16th.)
+template <class T, bool WIDE>
+struct Columns {
+    static constexpr bool SPREAD = !WIDE && sizeof(T) == 4;
+    static constexpr int STEP = SPREAD ? 16 : 1;
+    static __device__ __forceinline__ int first(int b, int lane) { return b * kScaleBlock + lane * (SPREAD ? 1 : 8); }
+};
+
+// the lane's values of a block of a source row, or of its SwiGLU; zeros for no row
 template <class T, bool SWIGLU, bool WIDE>
-__device__ __forceinline__ void row_values(const T *x, int c0, int cols, float (&v)[8])
+__device__ __forceinline__ void row_values(const T *x, int b, int lane, int cols, float (&v)[8])
 {
-    if (!x) {
+    const int c0 = Columns<T, WIDE>::first(b, lane);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.f;
-        return;
+    for (int j = 0; j < 8; ++j) {
+        const int c = c0 + j * Columns<T, WIDE>::STEP;
+        v[j] = x && c < cols ? as_float(x[c]) : 0.f;
     }
-    load_values<T, WIDE>(x, c0, cols, v);
     if (SWIGLU) {
         float w[8];
-        load_values<T, WIDE>(x + cols, c0, cols, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = c0 + j * Columns<T, WIDE>::STEP;
+            w[j] = x && c < cols ? as_float(x[cols + c]) : 0.f;
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = silu(v[j]) * w[j];
     }
 }
 
-// the lane's eight values of block b of `row`
+template <class T, bool WIDE>
 __device__ __forceinline__ void store_codes(const QuantArgs &a, const float (&v)[8], float inv, int row, int b, int lane)
 {
     uint2 q;
     q.x = e4m3x2(v[0] * inv, v[1] * inv) | e4m3x2(v[2] * inv, v[3] * inv) << 16;
     q.y = e4m3x2(v[4] * inv, v[5] * inv) | e4m3x2(v[6] * inv, v[7] * inv) << 16;
-    const int c0 = b * kScaleBlock + lane * 8;
-    uint8_t *dst = a.codes + (int64_t)row * a.ld_codes + c0;
-    if (c0 + 8 <= a.cols) {
-        *reinterpret_cast<uint2 *>(dst) = q;
+    const int c0 = Columns<T, WIDE>::first(b, lane);
+    uint8_t *dst = a.codes + (int64_t)row * a.ld_codes;
+    if (!Columns<T, WIDE>::SPREAD && c0 + 8 <= a.cols) {
+        *reinterpret_cast<uint2 *>(dst + c0) = q;
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c0 + j < a.cols) dst[j] = (uint8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+        for (int j = 0; j < 8; ++j) {
+            const int c = c0 + j * Columns<T, WIDE>::STEP;
+            if (c < a.cols) dst[c] = (uint8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+        }
     }
 }
 
@@ -212,8 +229,8 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const Quan
                 }
             }
         } else {
-            row_values<T, SWIGLU, WIDE>(x, b0 * kScaleBlock + lane * 8, a.cols, v0);
-            row_values<T, SWIGLU, WIDE>(x, b1 * kScaleBlock + lane * 8, a.cols, v1);
+            row_values<T, SWIGLU, WIDE>(x, b0, lane, a.cols, v0);
+            row_values<T, SWIGLU, WIDE>(x, b1, lane, a.cols, v1);
         }
         const bool second = lane & 8;
         const float m0 = amax8(v0), m1 = amax8(v1);
@@ -224,8 +241,8 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const Quan
         block_scale(m, scale, inv);
         const float inv0 = __shfl_sync(0xffffffffu, inv, 0, 16), inv1 = __shfl_sync(0xffffffffu, inv, 8, 16);
         if (row >= a.rows) continue;
-        store_codes(a, v0, inv0, row, b0, lane);
-        if (b1 < a.blocks) store_codes(a, v1, inv1, row, b1, lane);
+        store_codes<T, WIDE>(a, v0, inv0, row, b0, lane);
+        if (b1 < a.blocks) store_codes<T, WIDE>(a, v1, inv1, row, b1, lane);
         const int b = second ? b1 : b0;
         if ((lane & 7) == 0 && b < a.blocks) a.scales[(int64_t)b * a.ld_scales + row] = scale;
     }
