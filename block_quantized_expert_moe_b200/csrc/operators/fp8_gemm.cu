@@ -28,6 +28,10 @@
 // Few tiles (decode): the K blocks of a tile are split over the CTAs of a
 // cluster, whose partial sums meet through distributed shared memory in rank
 // order: no workspace, no atomics, the same bits every run.
+// Decode batches are bound by the weights' bytes: 64 tokens over 512 experts of 1024 x
+// 2048 (352 read on average) 108.5 us, 6.8 TB/s.  Single tokens are bound by latency:
+// one token's ten experts (20 MB) 9.7 us, one row x 1024 x 2048 4.1 us (group table
+// 1.1 us when its offsets are cold, first tile 2 us, exchange 1.5 us).
 // Every mbarrier wait is bounded.
 #include "fp8_common.cuh"
 

@@ -19,6 +19,12 @@
 // the kernel for few rows, every column has a scale of its own, read from shared memory:
 // 153.7 us at 8192 x 4096 x 4096.)
 //
+// 8192 x 4096 x 4096 takes 122 us, 2.26 PFLOP/s, and 143 us (1.92) in a loop of a second:
+// the power cap holds the SMs at 1.5 to 1.7 GHz, without the epilogue's work the same
+// loop runs 105 us, with one of the four instructions a block 108.  81,920 rows over 512
+// experts of 1024 x 2048 take 330 us (weights alone 163 us of HBM): each expert's 160
+// rows fill 62 % of its tile.
+//
 //   warps 0-7    epilogue: warpgroup h owns columns 128 h .. 128 h + 127
 //   warp 8       TMA producer (both CTAs; all bytes count on the leader's barrier)
 //   warp 9       MMA issuer (the leader's only)
