@@ -17,16 +17,24 @@ _MASKS = (torch.bool, torch.uint8)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _tensor(t, name, dtypes, shape):
-    """A contiguous tensor of one of `dtypes` and of `shape`."""
+def _refuse(t, name, dtypes, shape):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor, not {type(t).__name__}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, not {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+
+
+def _tensor(t, name, dtypes, shape):
+    """A contiguous tensor of one of `dtypes` and of `shape`."""
+    try:
+        if t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _refuse(t, name, dtypes, shape)
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _shape(t, name, dims):
@@ -38,7 +46,7 @@ def _shape(t, name, dims):
 
 def _float_code(t, name):
     code = _FLOAT_CODE.get(getattr(t, "dtype", None))
-    if code is None or not isinstance(t, torch.Tensor):
+    if code is None:
         raise TypeError(f"{name} must be a torch.float32 or torch.bfloat16 tensor, not "
                         f"{getattr(t, 'dtype', type(t).__name__)}")
     return code
@@ -46,21 +54,20 @@ def _float_code(t, name):
 
 def _rows(t, name, dtypes, shape):
     """A tensor whose rows are contiguous and do not overlap; returns the row stride."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor, not {type(t).__name__}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, not {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     cols = shape[-1]
-    stride = t.stride()
-    if stride[-1] != 1 and cols > 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-    if shape[-2] <= 1:
-        return cols  # one row (or none): its stride is never used
-    if stride[-2] < cols:
-        raise ValueError(f"{name}'s rows must not overlap")
-    return stride[-2]
+    try:
+        if t.dtype in dtypes and t.shape == shape:
+            stride = t.stride()
+            if stride[-1] == 1 or cols <= 1:
+                if shape[-2] <= 1:
+                    return cols  # one row (or none): its stride is never used
+                if stride[-2] >= cols:
+                    return stride[-2]
+                raise ValueError(f"{name}'s rows must not overlap")
+            raise ValueError(f"{name}'s last dimension must be contiguous")
+    except AttributeError:
+        pass
+    _refuse(t, name, dtypes, shape)
 
 
 def _code_rows(t, name, shape):
@@ -74,16 +81,23 @@ def _code_rows(t, name, shape):
     return ld
 
 
+def _off_device(names, tensors, device):
+    for name, t in zip(names, tensors):
+        if t is not None:
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor: the library reads and writes device memory")
+            if t.get_device() != device:
+                raise ValueError(f"{name} is on cuda:{t.get_device()}, expected cuda:{device}")
+
+
 def _run(fn, names, tensors, args, stream):
     """Checks that every tensor is on one CUDA device, then calls fn(*args, stream) with that device current."""
     device = tensors[0].get_device()
-    for i, t in enumerate(tensors):
-        if t is not None:
-            d = t.get_device()
-            if d < 0 or not t.is_cuda:
-                raise ValueError(f"{names[i]} must be a CUDA tensor: the library reads and writes device memory")
-            if d != device:
-                raise ValueError(f"{names[i]} is on cuda:{d}, expected cuda:{device}")
+    for t in tensors:
+        if t is not None and t.get_device() != device or device < 0:
+            _off_device(names, tensors, device)
+    if not tensors[0].is_cuda:
+        _off_device(names, tensors, device)
     if stream is None:
         s = _raw_stream(device) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
     else:
