@@ -44,7 +44,7 @@ struct Raw;
 template <>
 struct Raw<float, 4> {
     float4 r;
-    __device__ __forceinline__ void load(const float *p) { r = __ldg(reinterpret_cast<const float4 *>(p)); }
+    __device__ __forceinline__ void load(const float *p) { r = *reinterpret_cast<const float4 *>(p); }
     __device__ __forceinline__ void fill() { r = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
     __device__ __forceinline__ void values(float *v) const { v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w; }
     static __device__ __forceinline__ void store(float *p, const float *v)
@@ -55,7 +55,7 @@ struct Raw<float, 4> {
 template <>
 struct Raw<__nv_bfloat16, 8> {
     uint4 r;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { r = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { r = *reinterpret_cast<const uint4 *>(p); }
     __device__ __forceinline__ void fill() { r = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
     __device__ __forceinline__ void values(float *v) const
     {
@@ -80,7 +80,7 @@ struct Raw<__nv_bfloat16, 8> {
 template <>
 struct Raw<float, 1> {
     float r;
-    __device__ __forceinline__ void load(const float *p) { r = __ldg(p); }
+    __device__ __forceinline__ void load(const float *p) { r = *p; }
     __device__ __forceinline__ void fill() { r = -INFINITY; }
     __device__ __forceinline__ void values(float *v) const { v[0] = r; }
     static __device__ __forceinline__ void store(float *p, const float *v) { *p = v[0]; }
@@ -276,8 +276,8 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_forward_kernel(const B
     bool next_valid = true;
     const auto fetch = [&](int row) {
         next.load(logits + (size_t)row * a.E, a.E, lane);
-        next_valid = !a.valid || __ldg(a.valid + row);
-        next_choice = lane < a.k ? __ldg(a.idx + (size_t)row * a.k + lane) : -1;
+        next_valid = !a.valid || a.valid[row];
+        next_choice = lane < a.k ? a.idx[(size_t)row * a.k + lane] : -1;
     };
     if (t < a.T) fetch(t);
     for (; t < a.T; t += step) {
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_forward_kernel(const B
         ++n_valid;
         if ((unsigned)choice < (unsigned)a.E) atomicAdd(&hist[choice], 1);
         for (int j = 32 + lane; j < a.k; j += 32) {
-            const int e = __ldg(a.idx + (size_t)t * a.k + j);
+            const int e = a.idx[(size_t)t * a.k + j];
             if ((unsigned)e < (unsigned)a.E) atomicAdd(&hist[e], 1);
         }
         row_softmax<NV>(v);
@@ -336,22 +336,22 @@ constexpr int kBwdWarps = 8, kBwdThreads = 32 * kBwdWarps;
 
 template <class T, int NV, int V>
 __global__ void __launch_bounds__(kBwdThreads)
-    balance_backward_kernel(const T *__restrict__ logits, const int32_t *__restrict__ counts,
-                            const uint8_t *__restrict__ valid, const float *__restrict__ dloss, int tokens, int E, int k,
-                            T *__restrict__ dlogits)
+    balance_backward_kernel(const T *logits, const int32_t *counts,
+                            const uint8_t *valid, const float *dloss, int tokens, int E, int k,
+                            T *dlogits)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     follow_previous();
-    const double n = (double)max(__ldg(counts + E), 1);
+    const double n = (double)max(counts[E], 1);
     const float to_share = (float)((double)E / ((double)k * n));
-    const float scale = __ldg(dloss) / (float)n;
+    const float scale = *dloss / (float)n;
     float f[NV];
 #pragma unroll
     for (int i = 0; i < NV / V; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int c = (i * 32 + lane) * V + j;
-            f[i * V + j] = c < E ? (float)__ldg(counts + c) * to_share : 0.f;
+            f[i * V + j] = c < E ? (float)counts[c] * to_share : 0.f;
         }
     // (a row ahead in registers costs more warps than it hides: 30.6 against 46.4 us at 65,536 x 512)
     for (int t = blockIdx.x * kBwdWarps + warp; t < tokens; t += gridDim.x * kBwdWarps) {
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kBwdThreads)
         Row<T, NV, V> row;
         row.load(logits + (size_t)t * E, E, lane);  // not held up by the mask
         row.values(v);
-        if (!valid || __ldg(valid + t)) {
+        if (!valid || valid[t]) {
             row_softmax<NV>(v);
             float dot = 0.f;
 #pragma unroll

@@ -37,7 +37,7 @@ constexpr int kPlanCluster = 16;  // beyond the portable 8: checked when the ker
 
 __device__ __forceinline__ int load_choice(const int32_t *idx, int p, int end, int E)
 {
-    const int e = p < end ? __ldg(idx + p) : -1;
+    const int e = p < end ? idx[p] : -1;
     return (unsigned)e < (unsigned)E ? e : -1;
 }
 
@@ -56,8 +56,8 @@ __device__ __forceinline__ unsigned same_choice(int e, int bits)
 }
 
 __global__ void __launch_bounds__(kPlanThreads, 1)
-    expert_plan_kernel(const int32_t *__restrict__ idx, int P, int k, int E, int bits, int warps, int32_t *__restrict__ counts,
-                       int32_t *__restrict__ offsets, int32_t *__restrict__ rows, int32_t *__restrict__ slots)
+    expert_plan_kernel(const int32_t *idx, int P, int k, int E, int bits, int warps, int32_t *counts,
+                       int32_t *offsets, int32_t *rows, int32_t *slots)
 {
     extern __shared__ int32_t smem[];
     int32_t *total = smem;           // [E] this CTA's pairs per expert (read by the cluster)

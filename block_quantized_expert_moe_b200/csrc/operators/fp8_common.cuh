@@ -161,7 +161,7 @@ __device__ __forceinline__ void build_groups(const ProductArgs &a, int bn, int *
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int g = i * THREADS + threadIdx.x;
-        raw[i] = g <= a.groups ? __ldg(a.offsets + g) : 0;
+        raw[i] = g <= a.groups ? a.offsets[g] : 0;
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {

@@ -234,10 +234,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i) {
                     const int kb = min(k0 + i, kb1 - 1);
-                    w[i] = __ldg(bs + kb);
+                    w[i] = bs[kb];
 #pragma unroll
                     for (int j = 0; j < PER; ++j)
-                        v[i][j] = __ldg(a.a_scale + (int64_t)kb * a.ld_a_scale + t.row0 + min(j * 32 + lane, t.rows - 1));
+                        v[i][j] = *(a.a_scale + (int64_t)kb * a.ld_a_scale + t.row0 + min(j * 32 + lane, t.rows - 1));
                 }
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i) {

@@ -136,7 +136,7 @@ __device__ __forceinline__ void columns_wait() { asm volatile("tcgen05.wait::ld.
 __device__ __forceinline__ float load_ahead(const float *p)
 {
     float v;
-    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
     return v;
 }
 

@@ -84,8 +84,8 @@ struct Raw8<float> {
     float4 a, b;
     __device__ __forceinline__ void load(const float *p)
     {
-        a = __ldg(reinterpret_cast<const float4 *>(p));
-        b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+        a = *reinterpret_cast<const float4 *>(p);
+        b = reinterpret_cast<const float4 *>(p)[1];
     }
     __device__ __forceinline__ void values(float (&v)[8]) const
     {
@@ -95,7 +95,7 @@ struct Raw8<float> {
 template <>
 struct Raw8<__nv_bfloat16> {
     uint4 r;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { r = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { r = *reinterpret_cast<const uint4 *>(p); }
     __device__ __forceinline__ void values(float (&v)[8]) const
     {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const Quan
     follow_previous();
     const T *x = nullptr;
     if (row < a.rows) {
-        const int src = a.index ? __ldg(a.index + row) : row;
+        const int src = a.index ? a.index[row] : row;
         if ((unsigned)src < (unsigned)a.src_rows) x = static_cast<const T *>(a.x) + (int64_t)src * a.ld_x;
     }
     for (int b0 = half / kQuantRows + blockIdx.y * kQuantTurn; b0 < a.blocks; b0 += kQuantTurn * gridDim.y) {
@@ -253,9 +253,9 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const Quan
 // One CTA per 128 x 128 block: thread t holds 8 columns of rows t / 16 + 16 i.
 template <class T, bool WIDE>
 __global__ void __launch_bounds__(kQuantThreads)
-    quantize_weight_kernel(const T *__restrict__ w, int64_t ld_w, int64_t group_stride, int n, int cols,
-                           uint8_t *__restrict__ codes, int64_t ld_codes, int64_t codes_stride,
-                           float *__restrict__ scales)
+    quantize_weight_kernel(const T *w, int64_t ld_w, int64_t group_stride, int n, int cols,
+                           uint8_t *codes, int64_t ld_codes, int64_t codes_stride,
+                           float *scales)
 {
     __shared__ float red[kQuantThreads / 32];
     const int kb = blockIdx.x, nb = blockIdx.y, g = blockIdx.z;
