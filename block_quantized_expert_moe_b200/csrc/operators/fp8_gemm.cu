@@ -30,8 +30,8 @@
 // order: no workspace, no atomics, the same bits every run.
 // Decode batches are bound by the weights' bytes: 64 tokens over 512 experts of 1024 x
 // 2048 (352 read on average) 108.5 us, 6.8 TB/s.  Single tokens are bound by latency:
-// one token's ten experts (20 MB) 9.7 us, one row x 1024 x 2048 4.1 us (group table
-// 1.1 us when its offsets are cold, first tile 2 us, exchange 1.5 us).
+// one token's ten experts (20 MB) 9.3 us, one row x 1024 x 2048 4.2 us (group table
+// 1.1 us when its offsets are cold, first tile 2 us, exchange 1 us).
 // Every mbarrier wait is bounded.
 #include "fp8_common.cuh"
 
@@ -52,7 +52,7 @@ struct Config {
     static constexpr int STAGE_BYTES = kABytes + BN * 128;
     static constexpr int TABLE = 2 * (kMaxExperts + 1) * 4;  // group offsets, first tiles
     static constexpr int SMEM = STAGES * STAGE_BYTES + kScales * BN * 4 + TABLE + 1024;
-    static_assert(STAGES * STAGE_BYTES >= kWeightRows * BN * 4, "partial tile fits the operand ring");
+    static constexpr int PARTIAL = kWeightRows * BN * 4;  // partial sums of the cluster's ranks (K split)
     static_assert(2 * (SMEM + 2048) <= 228 * 1024, "two CTAs an SM");
 };
 typedef Config<64, 4> Narrow;
@@ -97,28 +97,29 @@ __device__ __forceinline__ void fma_pair(float2 &acc, uint32_t v0, uint32_t v1, 
         : "r"(v0), "r"(v1), "f"(s0), "f"(s1));
 }
 
-// This rank's columns of the tile: the cluster's partial sums in rank order, 32 of them in
-// flight.
-template <class C, int RANKS, class OUT>
-__device__ __forceinline__ void add_partials(uint32_t own, int rank, int cols, OUT *out, int64_t ld)
+__device__ __forceinline__ void cluster_st_f32(uint32_t addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// This thread's weight row of this rank's columns: the ranks' partial sums [rank][per][row] in
+// rank order, 32 loads in flight.
+template <int RANKS, class OUT>
+__device__ __forceinline__ void add_partials(const float *p, int per, int cols, OUT *out, int64_t step)
 {
     constexpr int N = 32 / RANKS;
 #pragma unroll 1
-    for (int c0 = rank; c0 < cols; c0 += N * RANKS) {
-        float p[N][RANKS];
+    for (int c = 0; c < cols; c += N, p += N * kWeightRows, out += N * step) {
+        float v[N][RANKS];
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
-            for (int r = 0; r < RANKS; ++r) {
-                p[i][r] = 0.f;
-                if (c0 + i * RANKS < cols) p[i][r] = cluster_ld_f32(cluster_map(own + (c0 + i * RANKS) * kWeightRows * 4, r));
-            }
+            for (int r = 0; r < RANKS; ++r) v[i][r] = c + i < cols ? p[(r * per + i) * kWeightRows] : 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            float v = p[i][0];
 #pragma unroll
-            for (int r = 1; r < RANKS; ++r) v += p[i][r];
-            if (c0 + i * RANKS < cols) out[(int64_t)(c0 + i * RANKS) * ld] = OUT(v);
+            for (int r = 1; r < RANKS; ++r) v[i][0] += v[i][r];
+            if (c + i < cols) out[i * step] = OUT(v[i][0]);
         }
     }
 }
@@ -138,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     float *scale_ring = reinterpret_cast<float *>(smem + C::STAGES * C::STAGE_BYTES);
     int *offset = reinterpret_cast<int *>(scale_ring + kScales * C::BN);
     int *first_tile = offset + kMaxExperts + 1;
+    float *partial = reinterpret_cast<float *>(first_tile + kMaxExperts + 1);  // [rank][column][weight row], if ranks > 1
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned rank = cluster_rank(), ranks = cluster_size();
 
@@ -295,31 +297,33 @@ __global__ void __launch_bounds__(kThreads, 2)
         __syncwarp();
         if (!go) abort_flag = 1;
         if (ranks > 1) {
-            // partial sums of the cluster's CTAs, added in rank order; the operand ring is
-            // idle here (its last block has been multiplied) and holds this CTA's partial
-            float *partial = reinterpret_cast<float *>(smem);  // [column][weight row]
+            // Column c of the tile belongs to rank c % ranks: every rank sends its partial sums there,
+            // and after one barrier the owner adds them in rank order from its own shared memory
+            // (reading them from the others' instead costs 2 us more).
+            const int per = (ncols + (int)ranks - 1) >> shift;  // columns of a rank
             if (warp < kEpiWarps) {
-                const int m = threadIdx.x;
+                const uint32_t own = smem_u32(partial + (rank * per * kWeightRows + threadIdx.x));
 #pragma unroll
                 for (int i = 0; i < C::BN / 2; ++i) {
                     if (2 * i < ncols) {
-                        partial[2 * i * kWeightRows + m] = acc[i].x;
-                        partial[(2 * i + 1) * kWeightRows + m] = acc[i].y;
+                        cluster_st_f32(cluster_map(own + (2 * i >> shift) * (kWeightRows * 4), 2 * i & (ranks - 1)), acc[i].x);
+                        cluster_st_f32(cluster_map(own + ((2 * i + 1) >> shift) * (kWeightRows * 4), (2 * i + 1) & (ranks - 1)),
+                                       acc[i].y);
                     }
                 }
             }
             cluster_sync();
-            if (warp < kEpiWarps && !abort_flag) {
-                const int n = t.n_tile * kWeightRows + (int)threadIdx.x;
-                OUT *out = static_cast<OUT *>(a.out) + (int64_t)t.row0 * a.ld_out + n;
-                const uint32_t own = smem_u32(partial + threadIdx.x);
-                const int cols = n < a.n ? t.rows : 0;
-                if (ranks == 2) add_partials<C, 2>(own, (int)rank, cols, out, a.ld_out);
-                else if (ranks == 4) add_partials<C, 4>(own, (int)rank, cols, out, a.ld_out);
-                else add_partials<C, 8>(own, (int)rank, cols, out, a.ld_out);
+            const int n = t.n_tile * kWeightRows + (int)threadIdx.x;
+            if (warp < kEpiWarps && !abort_flag && n < a.n) {
+                OUT *out = static_cast<OUT *>(a.out) + (int64_t)(t.row0 + (int)rank) * a.ld_out + n;
+                const float *p = partial + threadIdx.x;
+                const int cols = (t.rows - (int)rank + (int)ranks - 1) >> shift;  // may be none
+                const int64_t step = ranks * a.ld_out;
+                if (ranks == 2) add_partials<2>(p, per, cols, out, step);
+                else if (ranks == 4) add_partials<4>(p, per, cols, out, step);
+                else add_partials<8>(p, per, cols, out, step);
             }
-            fence_proxy_async_smem();  // the ring is written by TMA again
-            cluster_sync();
+            if (id + workers < n_work) cluster_sync();  // the next tile's sums may come
         } else if (warp < kEpiWarps && !abort_flag) {
             const int n = t.n_tile * kWeightRows + (int)threadIdx.x;
             if (n < a.n) {
@@ -347,9 +351,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 template <class C>
 cudaError_t set_smem()
 {
-    cudaError_t e = cudaFuncSetAttribute(fp8_product_kernel<C, float>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(fp8_product_kernel<C, float>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM + C::PARTIAL);
     if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(fp8_product_kernel<C, __nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    return cudaFuncSetAttribute(fp8_product_kernel<C, __nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM + C::PARTIAL);
 }
 
 template <class C>
@@ -360,9 +364,10 @@ moe_status run_product(const Operands &o, const ProductArgs &a, moe_dtype out_dt
     if (!code_map(&mw, o.b, o.k, a.n, o.ld_b, a.groups, o.stride_b, kWeightRows)) return MOE_ERR_CUDA;
     if (!code_map(&mx, o.a, o.k, a.rows, o.ld_a, 0, 0, kBox)) return MOE_ERR_CUDA;
     const dim3 grid(workers * ranks);
-    return launched(out_dtype == MOE_DT_BF16 ? launch(fp8_product_kernel<C, __nv_bfloat16>, grid, kThreads, C::SMEM, s,
+    const int smem = C::SMEM + (ranks > 1 ? C::PARTIAL : 0);
+    return launched(out_dtype == MOE_DT_BF16 ? launch(fp8_product_kernel<C, __nv_bfloat16>, grid, kThreads, smem, s,
                                                       ranks, mw, mx, a)
-                                             : launch(fp8_product_kernel<C, float>, grid, kThreads, C::SMEM, s, ranks,
+                                             : launch(fp8_product_kernel<C, float>, grid, kThreads, smem, s, ranks,
                                                       mw, mx, a));
 }
 
@@ -427,7 +432,7 @@ moe_status product(const uint8_t *a, int64_t ld_a, const float *a_scale, int64_t
     // both read every weight once (128 experts of 1024 x 2048, pair against narrow: 32 rows 73.1 /
     // 59.9 us, 48 rows 74.8 / 68.0, 64 rows 76.4 / 76.7, 128 rows 88.4 / 123.7; 512 experts of 2048 x
     // 512, 40 rows 188 / 168).  Few waves: by the blocks that the busiest CTA takes one after another,
-    // 0.5 us each for a pair, 0.65 us for a narrow tile alone on its SM and 0.9 us for two, and 2 us for
+    // 0.5 us each for a pair, 0.65 us for a narrow tile alone on its SM and 0.9 us for two, and 1 us for
     // a cluster's exchange (rows x n x k, pair / narrow: 128 x 4096 x 4096 17.8 / 15.7 us, 256 x 4096 x
     // 4096 18.9 / 22.8, 1024 x 4096 x 4096 20.5 / 54.5, 256 x 1024 x 2048 12.1 / 8.9, 1024 x 1024 x 1024
     // 9.1 / 10.3, 4096 x 512 x 512 7.6 / 10.4; 8 experts of 2048 x 2048, 64 rows 14.5 / 18.2).
@@ -437,7 +442,7 @@ moe_status product(const uint8_t *a, int64_t ld_a, const float *a_scale, int64_t
     } else {
         const int64_t pair_cost = 10 * (int64_t)p.kblocks * ceil_div(wide, pairs) + 20;  // in 50 ns
         const int64_t each = (narrow * ranks > sms ? 18 : 13) * (int64_t)ceil_div(p.kblocks, ranks);
-        pair = pair && pair_cost < each * ceil_div(narrow * ranks, slots) + (ranks > 1 ? 40 : 0);
+        pair = pair && pair_cost < each * ceil_div(narrow * ranks, slots) + (ranks > 1 ? 20 : 0);
     }
     if (pair) return pair_product(o, p, out_dtype, (int)std::min<int64_t>(wide, pairs), s);
     const int workers = (int)std::min<int64_t>(narrow, slots / ranks);
