@@ -97,11 +97,6 @@ __device__ __forceinline__ void fma_pair(float2 &acc, uint32_t v0, uint32_t v1, 
         : "r"(v0), "r"(v1), "f"(s0), "f"(s1));
 }
 
-__device__ __forceinline__ void cluster_st_f32(uint32_t addr, float v)
-{
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-
 // This thread's weight row of this rank's columns: the ranks' partial sums [rank][per][row] in
 // rank order, 32 loads in flight.
 template <int RANKS, class OUT>
@@ -164,11 +159,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         abort_flag = 0;
         fence_mbar_init();
     }
+    __syncwarp();
+    if (ranks > 1) cluster_started();
     follow_previous();
     build_groups<kThreads>(a, C::BN, offset, first_tile, warp_tiles);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
+    if (ranks > 1) cluster_wait_started();
     const uint32_t tmem = tmem_base;
     const int n_work = first_tile[a.groups] * a.n_tiles;
     const int shift = 31 - __clz(ranks);  // 1, 2, 4 or 8 ranks

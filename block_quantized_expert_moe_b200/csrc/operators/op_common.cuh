@@ -99,6 +99,19 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// A CTA's shared memory may be written by the others once it has started: each arrives when
+// it starts and waits before it sends.  (All threads of a converged warp; waits for residents of
+// one cluster, which are scheduled together.)
+__device__ __forceinline__ void cluster_started()
+{
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait_started()
+{
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+
 // The shared::cluster address in CTA `rank` of a shared-memory address of this CTA.
 __device__ __forceinline__ uint32_t cluster_map(uint32_t addr, unsigned rank)
 {
@@ -112,6 +125,16 @@ __device__ __forceinline__ uint32_t cluster_ld_u32(uint32_t addr)
     uint32_t v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
+}
+
+__device__ __forceinline__ void cluster_st_u32(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void cluster_st_f32(uint32_t addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 __device__ __forceinline__ float cluster_ld_f32(uint32_t addr)
