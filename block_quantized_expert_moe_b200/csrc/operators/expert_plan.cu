@@ -19,8 +19,8 @@
 //
 // The work is latency: 12 bytes a pair (index read, slot and row written).  A
 // cluster of 16 CTAs takes prefill chunks, one CTA the decode batches.  With 10
-// choices among 512 experts: 8 tokens 3.0 us, 512 tokens 7.4, 8,192 tokens 12.5,
-// 65,536 tokens 62 (there bound by the scattered row writes of 16 SMs).
+// choices among 512 experts: 8 tokens 3.1 us, 512 tokens 6.1, 8,192 tokens 12.1,
+// 65,536 tokens 62 (there half of it ballots, half the second pass, of 16 SMs).
 #include <algorithm>
 
 #include "op_common.cuh"
@@ -32,7 +32,7 @@ using namespace op;
 
 constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanBatch = 8;  // index loads in flight per lane
-constexpr int kPlanPairsOfOne = 2560;  // 7.5 us with one CTA and with a cluster; more pairs take a cluster
+constexpr int kPlanPairsOfOne = 2048;  // one CTA / a cluster: 1,280 pairs 4.9 / 6.0 us, 2,560 6.6 / 6.1
 constexpr int kPlanCluster = 16;  // beyond the portable 8: checked when the kernel is prepared
 
 __device__ __forceinline__ int load_choice(const int32_t *idx, int p, int end, int E)
@@ -60,18 +60,19 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
                        int32_t *offsets, int32_t *rows, int32_t *slots)
 {
     extern __shared__ int32_t smem[];
-    int32_t *total = smem;           // [E] this CTA's pairs per expert (read by the cluster)
-    int32_t *base = total + E;       // [E] first slot of this CTA's pairs of each expert
-    int32_t *hist = base + E;        // [warps][E]
+    int32_t *base = smem;                       // [E] first slot of this CTA's pairs of each expert
+    int32_t *total = base + E;                  // [CTA of the cluster][E] pairs per expert, sent by each
+    int32_t *hist = total + cluster_size() * E;  // [warps][E]
     __shared__ int32_t warp_sum[kPlanWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned rank = cluster_rank(), ctas = cluster_size();
 
-    const int words = warps * E;  // the histograms start on 16 bytes where E is a multiple of 2
-    if ((E & 1) == 0) {
+    if (ctas > 1) cluster_started();
+
+    const int words = warps * E;  // the histograms start on 16 bytes where E is a multiple of 4
+    if ((E & 3) == 0) {
         int4 *h4 = reinterpret_cast<int4 *>(hist);
         for (int i = threadIdx.x; i < words / 4; i += kPlanThreads) h4[i] = make_int4(0, 0, 0, 0);
-        if (threadIdx.x < (words & 3)) hist[(words & ~3) + threadIdx.x] = 0;
     } else {
         for (int i = threadIdx.x; i < words; i += kPlanThreads) hist[i] = 0;
     }
@@ -102,6 +103,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     }
     __syncthreads();
 
+    if (ctas > 1) cluster_wait_started();
+
     // over the CTA's warps: hist becomes the pairs of earlier warps
     for (int e = threadIdx.x; e < E; e += kPlanThreads) {
         int run = 0;
@@ -115,7 +118,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
                 run += n[w];
             }
         }
-        total[e] = run;
+        if (ctas > 1) {  // every CTA gets every CTA's totals (reading them there costs 1.3 us more)
+            const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(total + rank * E + e));
+            for (unsigned c = 0; c < ctas; ++c) cluster_st_u32(cluster_map(at, c), run);
+        } else {
+            total[e] = run;
+        }
     }
     if (ctas > 1) cluster_sync();
     else __syncthreads();
@@ -123,18 +131,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     // over the cluster, then over the experts (E <= the block's threads)
     int all = 0, before = 0;
     if (threadIdx.x < E) {
-        if (ctas > 1) {
-            const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(total + threadIdx.x));
-            int n[kPlanCluster];
-#pragma unroll
-            for (unsigned c = 0; c < kPlanCluster; ++c) n[c] = c < ctas ? (int)cluster_ld_u32(cluster_map(a, c)) : 0;
-#pragma unroll
-            for (unsigned c = 0; c < kPlanCluster; ++c) {
-                if (c < rank) before += n[c];
-                all += n[c];
-            }
-        } else {
-            all = total[threadIdx.x];
+        for (unsigned c = 0; c < ctas; ++c) {
+            const int n = total[c * E + threadIdx.x];
+            if (c < rank) before += n;
+            all += n;
         }
     }
     int scan = all;
@@ -187,10 +187,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     // rows behind the last group belong to no token
     for (int64_t s = used + (int64_t)rank * kPlanThreads + threadIdx.x; s < P; s += (int64_t)ctas * kPlanThreads)
         rows[s] = -1;
-    if (ctas > 1) cluster_sync();  // `total` is read by the other CTAs until here
 }
 
-size_t plan_smem(int E, int warps) { return sizeof(int32_t) * (size_t)E * (2 + warps); }
+size_t plan_smem(int E, int warps, int ctas) { return sizeof(int32_t) * (size_t)E * (1 + ctas + warps); }
 
 PerDevice g_plan;
 int g_plan_cluster[kMaxDevices];  // largest cluster of the device, 16 or 8
@@ -201,7 +200,7 @@ cudaError_t plan_prepare()
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(expert_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)plan_smem(kMaxExperts, kPlanWarps));
+                                 (int)plan_smem(kMaxExperts, kPlanWarps, kPlanCluster));
     if (e == cudaSuccess) e = cudaFuncSetAttribute(expert_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
@@ -211,7 +210,7 @@ cudaError_t plan_prepare()
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(kPlanCluster);
     cfg.blockDim = dim3(kPlanThreads);
-    cfg.dynamicSmemBytes = plan_smem(kMaxExperts, kPlanWarps);
+    cfg.dynamicSmemBytes = plan_smem(kMaxExperts, kPlanWarps, kPlanCluster);
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int fit = 0;
@@ -250,7 +249,7 @@ extern "C" moe_status moe_expert_plan(const int32_t *idx, int n_tokens, int top_
         if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
         ctas = g_plan_cluster[dev];
     }
-    return launched(launch(expert_plan_kernel, dim3(ctas), kPlanThreads, plan_smem(n_experts, warps),
+    return launched(launch(expert_plan_kernel, dim3(ctas), kPlanThreads, plan_smem(n_experts, warps, ctas),
                            static_cast<cudaStream_t>(stream), ctas, idx, (int)pairs, top_k, n_experts, bits, warps,
                            counts, offsets, rows, slots));
 }
