@@ -268,7 +268,8 @@ def moe_fp8_quantize(x, codes, scales, rows=None, swiglu=False, stream=None):
         ld_s, one_s = scales.stride()
         dt = _FLOAT_CODE[x.dtype]
         plain = (W == (C + C if swiglu else C) and codes.dtype in _CODES and scales.dtype is _F32
-                 and scales.shape == ((C + 127) >> 7, R) and one_x == 1 and one_c == 1 and (one_s == 1 or R == 1) and ld_x >= W
+                 and scales.shape == ((C + 127) >> 7, R) and one_x == 1 and one_c == 1
+                 and (one_s == 1 or R == 1) and ld_x >= W
                  and ld_c >= C and not ld_c & 15 and ld_s >= R
                  and (S == R if rows is None else rows.dtype is _I32 and rows.shape == (R,) and rows.is_contiguous()))
     except _NOT_PLAIN:
