@@ -127,8 +127,15 @@ __device__ __forceinline__ void row_softmax(float (&v)[NV])
     for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     // fmaxf passes over NaN: those come back through 2^NaN below; with m = -inf subtract
     // 0 so that an empty row gives 2^-inf = 0.  exp(l - m) = 2^(l log2(e) - m log2(e)) in one
-    // FMA: the rounding of m log2(e) is the same for the whole row and cancels.
+    // FMA: the rounding of m log2(e) is a factor of the whole row, within 2^+-0.07 up to |m| = 2^20,
+    // and cancels.  Beyond that it could overflow (as m log2(e) itself does for a row of the
+    // type's lowest value): such rows, seldom enough, subtract first.
     constexpr float log2e = 1.44269504f;
+    if (fabsf(m) > 1048576.f && m != -INFINITY) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] -= m;
+        m = 0.f;
+    }
     const float shift = m == -INFINITY ? 0.f : -m * log2e;
     float s = 0.f;
 #pragma unroll

@@ -151,6 +151,36 @@ def test_balance_masked_experts_and_masked_rows():
         assert host(got[2])[3] == 0 and not host(got[3])[5].any()
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("E", [63, 64])
+def test_balance_of_logits_at_the_ends_of_the_type(E, dt):
+    """The softmax depends on differences alone: rows of only the lowest value are even, one largest value
+    takes its row, and large offsets change nothing.  Differences are 0 to 32, 64, or beyond 100 (p = 0)."""
+    t = DTYPES[dt]
+    lo, hi = torch.finfo(t).min, torch.finfo(t).max
+    g = torch.Generator(device="cuda").manual_seed(E)
+    logits = torch.zeros(12, E, device="cuda")
+    logits[0] = lo
+    logits[1] = lo
+    logits[1, ::2] = float("-inf")
+    logits[2] = hi
+    logits[3, 7] = hi
+    logits[4, :20], logits[4, 20:] = hi, lo
+    logits[5, :20], logits[5, 20:] = -1e30, lo
+    logits[6], logits[6, 5] = 1e30, -1e30
+    steps = torch.randint(0, 128, (5, E), generator=g, device="cuda")
+    logits[7] = 2.0 ** 21 + 0.25 * steps[0]
+    logits[8] = -(2.0 ** 21) - 0.25 * steps[1]
+    logits[9] = 2.0 ** 30 + 64 * (steps[2] % 3)
+    logits[10] = -(2.0 ** 30) - 64 * (steps[3] % 3)
+    logits[11] = 2.0 ** 19 + 0.25 * steps[4]
+    logits = logits.to(t)
+    idx = torch.randint(0, E, (12, 4), generator=g, device="cuda", dtype=torch.int32)
+    check_balance(logits, idx, None)
+    for row in range(12):  # each alone, where no other row hides its sum
+        check_balance(logits[row:row + 1].clone(), idx[row:row + 1].clone(), None)
+
+
 def test_balance_nan_reaches_the_loss_and_only_its_row_of_the_gradient():
     logits = torch.zeros(40, 64, device="cuda")
     logits[7, 3] = float("nan")
