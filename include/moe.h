@@ -438,8 +438,10 @@ size_t moe_balance_loss_workspace_bytes(int n_tokens, int n_experts);
  *             (NULL when that is 0); its contents need no initialisation.  Two
  *             calls that may run at the same time need one each.
  * 1 <= top_k <= n_experts <= 1024, n_tokens <= 2^30.  A logit of -inf has
- * probability 0; a token whose logits are all -inf adds nothing to P.  With no token that counts, loss, counts and P are 0.  Sums
- * are fp32 in a fixed order: results are reproducible bit for bit. */
+ * probability 0; a token whose logits are all -inf adds nothing to P; a NaN or
+ * +inf makes its token's probabilities NaN.  With no token that counts, loss,
+ * counts and P are 0.  Sums are fp32 in a fixed order: results are reproducible
+ * bit for bit. */
 moe_status moe_balance_loss(const void *logits, moe_dtype dtype, const int32_t *idx, const uint8_t *valid,
                             int n_tokens, int n_experts, int top_k, float *loss, int32_t *counts, float *prob_mean,
                             void *workspace, size_t workspace_bytes, void *stream);
@@ -488,7 +490,8 @@ moe_status moe_fp8_quantize_weight(const void *w, moe_dtype w_dtype, int64_t ld_
 
 /* out[r, j] = sum over blocks i of 128 columns of
  *   a_scale[i, r] * b_scale[j / 128, i] * sum_{c in block i} a[r, c] * b[j, c]
- * with fp32 sums, rounded once to the output's type.
+ * with fp32 sums, rounded once to the output's type; the product of the two scales is
+ * rounded to fp32 first.
  *   a        device [rows x k] E4M3 codes, row stride ld_a bytes
  *   a_scale  device [ceil(k / 128) x rows] fp32, row stride ld_a_scale
  *            elements (as moe_fp8_quantize writes them)
@@ -499,9 +502,9 @@ moe_status moe_fp8_quantize_weight(const void *w, moe_dtype w_dtype, int64_t ld_
  *            bounded wait of the kernel runs out (outputs are then undefined);
  *            otherwise it is not written
  * a and b are 16-byte aligned and their row strides multiples of 16; n and k
- * are any sizes up to 2^20, rows up to 2^30.  rows == 0 enqueues nothing.  The product by the
- * transposed weights (the gradient of a) is the same call on the transposed
- * codes and block scales. */
+ * are any sizes up to 2^20, rows up to 2^30.  rows == 0 enqueues nothing.  The
+ * product by the transposed weights (the gradient of a) is the same call on the
+ * transposed codes and block scales. */
 moe_status moe_fp8_matmul(const uint8_t *a, int64_t ld_a, const float *a_scale, int64_t ld_a_scale, int rows,
                           const uint8_t *b, int64_t ld_b, const float *b_scale, int n, int k, void *out,
                           moe_dtype out_dtype, int64_t ld_out, int32_t *status, void *stream);
@@ -509,8 +512,8 @@ moe_status moe_fp8_matmul(const uint8_t *a, int64_t ld_a, const float *a_scale, 
 /* Rows [offsets[g], offsets[g + 1]) times the transpose of matrix g.
  *   offsets  device [n_groups + 1] int32, ascending, within [0, rows] (as
  *            moe_expert_plan writes them; other values are clamped into that
- *            range).  Rows before the first and behind the last offset are not
- *            read and their outputs are left as they were.
+ *            range).  Rows before the first and behind the last offset do not
+ *            matter and their outputs are left as they were.
  *   b        device, n_groups matrices [n x k], group_stride_b bytes apart (a
  *            multiple of 16)
  *   b_scale  device [n_groups x ceil(n / 128) x ceil(k / 128)] fp32
