@@ -21,9 +21,10 @@
 // read of the logits but no saved tensor as large as they are.
 // Both are bound by the latency of their launches and of a row's two warp
 // reductions at the sizes of a training micro-batch (8,192 x 512 bf16, whose 8.4 MB
-// stay in L2: forward 10.5 us in two launches, backward 6.6 us), by launch latency
-// at decode sizes (64 x 64 fp32: 4.1 and 2.0 us); 65,536 x 512: 30.2 and 30.5 us,
-// 2.2 and 4.4 TB/s.
+// stay in L2: forward 10.0 us in two launches, backward 6.8 us), by launch latency
+// at decode sizes (64 x 64 fp32: 4.2 and 2.1 us); 65,536 x 512: 29.9 and 30.5 us,
+// 2.2 and 4.4 TB/s.  (Two rows of a warp at a time: 9.9 and 29.2 us forward, but 0.2 us
+// more up to 2,048 tokens.)
 #include <algorithm>
 
 #include "op_common.cuh"
@@ -305,12 +306,19 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_forward_kernel(const B
         for (int i = 0; i < NV; ++i) acc[i] += v[i];
     }
 #pragma unroll
-    for (int i = 0; i < NV / V; ++i)
+    for (int i = 0; i < NV / V; ++i) {
+        const int c = (i * 32 + lane) * V;
+        if (c >= a.E) continue;
+        float *col = warp_cols + warp * a.E + c;
+        if constexpr (V == 1) {
+            *col = acc[i];
+        } else {  // (E is a multiple of V; one value at a time all lanes meet in 32 / V banks: 0.75 us more)
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int c = (i * 32 + lane) * V + j;
-            if (c < a.E) warp_cols[warp * a.E + c] = acc[i * V + j];
+            for (int j = 0; j < V; j += 4)
+                *reinterpret_cast<float4 *>(col + j) =
+                    make_float4(acc[i * V + j], acc[i * V + j + 1], acc[i * V + j + 2], acc[i * V + j + 3]);
         }
+    }
     if (lane == 0 && n_valid) atomicAdd(&cta_valid, n_valid);
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += kBalThreads) {
