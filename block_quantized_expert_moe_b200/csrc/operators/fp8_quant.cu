@@ -34,6 +34,9 @@ constexpr int kQuantThreads = 256, kQuantRows = 8;
 // scale = a / 448 and inv = 448 / a, both correctly rounded.  The division by a constant is
 // Markstein's (IBM J. Res. Dev. 34, 1990): with c the rounded 1 / 448 and q = a c, one
 // exact residual corrects q to the rounded quotient; an infinite a is left as it is.
+// (x times the rounded 448 / a leaves a tie between two codes one fp32 step off in one of ten cases,
+// so that the odd code is taken, equally near; a second term of 448 / a mends that and costs 69.5 ->
+// 80.6 us for 81,920 gathered rows of 2048.)
 __device__ __forceinline__ void block_scale(float amax, float &scale, float &inv)
 {
     const float a = amax < kAmaxFloor ? kAmaxFloor : amax;  // NaN stays
