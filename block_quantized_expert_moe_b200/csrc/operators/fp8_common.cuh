@@ -139,9 +139,10 @@ struct TileWalk {
     }
 };
 
-// Groups' row offsets, clamped to an ascending sequence inside [0, rows], and each
-// group's first token tile of at most bn rows, in shared memory.  Every thread
-// of the CTA calls it; the caller synchronises afterwards.
+// Groups' row offsets, clamped to an ascending sequence inside [0, rows] (an offset below an
+// earlier one counts as that one, so that no row has two groups), and each group's first token
+// tile of at most bn rows, in shared memory.  Every thread of the CTA calls it; the caller
+// synchronises afterwards.
 template <int THREADS>
 __device__ __forceinline__ void build_groups(const ProductArgs &a, int bn, int *offset, int *first_tile, int *warp_tiles)
 {
@@ -172,13 +173,15 @@ __device__ __forceinline__ void build_groups(const ProductArgs &a, int bn, int *
     const int per = (a.groups + THREADS - 1) / THREADS;
     const int g0 = min(a.groups, (int)threadIdx.x * per), g1 = min(a.groups, g0 + per);
     int tiles[PER], sum = 0;
+    bool falls = false;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int g = g0 + i;
         tiles[i] = 0;
         if (g < g1) {
             const int lo = min(max(first_tile[g], 0), a.rows);
-            const int hi = min(max(first_tile[g + 1], lo), a.rows);
+            const int next = min(max(first_tile[g + 1], 0), a.rows), hi = max(next, lo);
+            falls = falls || next < lo;
             offset[g] = lo;
             if (g == a.groups - 1) offset[a.groups] = hi;
             tiles[i] = (hi - lo + bn - 1) / bn;
@@ -192,7 +195,22 @@ __device__ __forceinline__ void build_groups(const ProductArgs &a, int bn, int *
         if (lane >= d) scan += v;
     }
     if (lane == 31) warp_tiles[warp] = scan;
-    __syncthreads();
+    if (__syncthreads_or(falls)) {
+        // not a plan's offsets: one thread takes the running maximum
+        if (threadIdx.x == 0) {
+            int at = min(max(first_tile[0], 0), a.rows), count = 0;
+            for (int g = 0; g < a.groups; ++g) {
+                const int lo = at;
+                at = max(lo, min(first_tile[g + 1], a.rows));
+                offset[g] = lo;
+                first_tile[g] = count;
+                count += (at - lo + bn - 1) / bn;
+            }
+            offset[a.groups] = at;
+            first_tile[a.groups] = count;
+        }
+        return;
+    }
     int run = scan - sum;
     for (int w = 0; w < warp; ++w) run += warp_tiles[w];
 #pragma unroll

@@ -512,8 +512,9 @@ moe_status moe_fp8_matmul(const uint8_t *a, int64_t ld_a, const float *a_scale, 
 /* Rows [offsets[g], offsets[g + 1]) times the transpose of matrix g.
  *   offsets  device [n_groups + 1] int32, ascending, within [0, rows] (as
  *            moe_expert_plan writes them; other values are clamped into that
- *            range).  Rows before the first and behind the last offset do not
- *            matter and their outputs are left as they were.
+ *            range, and an offset below an earlier one counts as that one).
+ *            Rows before the first and behind the last offset do not matter
+ *            and their outputs are left as they were.
  *   b        device, n_groups matrices [n x k], group_stride_b bytes apart (a
  *            multiple of 16)
  *   b_scale  device [n_groups x ceil(n / 128) x ceil(k / 128)] fp32

@@ -1,0 +1,45 @@
+"""The operators beside the layer on the GPU where their definitions end: offsets that fall, values at
+the ends of a function's range, kernels that follow one another, waits that run out."""
+import numpy as np
+import pytest
+
+import op_reference as ref
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from test_gpu_operators import bq, check_groups, operands
+
+
+# 40 rows (the kernel for few rows) and many rows of every group (the kernel of CTA pairs)
+@pytest.mark.parametrize("offsets,R,N,K", [
+    ([0, 30, 10, 40], 40, 64, 128), ([35, 7, 7, -3, 36], 40, 130, 200), ([2 ** 31 - 1, 0, 5], 20, 64, 128),
+    ([-2 ** 31, 12, -2 ** 31, 2 ** 31 - 1], 14, 64, 300),
+    ([0, 900, 300, 2000, 1500, 1700, 4000], 4100, 512, 640),
+])
+def test_grouped_product_of_falling_offsets(offsets, R, N, K):
+    """An offset below an earlier one counts as that one: every row has one group, the results are those
+    of the running maximum and repeat."""
+    G = len(offsets) - 1
+    a, sa, b, sb = operands(R, N, K, 17, G)
+    want = np.maximum.accumulate(np.clip(offsets, 0, R))
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    before = torch.randn(R, N, device="cuda")
+    out = before.clone()
+    bq().moe_fp8_grouped_matmul(a, sa, b, sb, off, out)
+    check_groups(out, before, a, sa, b, sb, want, K)
+    for _ in range(5):
+        again = before.clone()
+        bq().moe_fp8_grouped_matmul(a, sa, b, sb, off, again)
+        assert torch.equal(out, again)
+
+
+def test_grouped_product_of_a_thousand_falling_offsets():
+    G, N, K, R = 1000, 64, 128, 3000
+    a, sa, b, sb = operands(R, N, K, 18, G)
+    offsets = np.random.default_rng(3).integers(-10, R + 10, G + 1)
+    offsets[: G // 2] = np.sort(offsets[: G // 2] // 4)
+    before = torch.zeros(R, N, device="cuda")
+    out = before.clone()
+    bq().moe_fp8_grouped_matmul(a, sa, b, sb, torch.from_numpy(offsets.astype(np.int32)).cuda(), out)
+    check_groups(out, before, a, sa, b, sb, np.maximum.accumulate(np.clip(offsets, 0, R)), K)
