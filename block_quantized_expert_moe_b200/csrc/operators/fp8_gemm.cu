@@ -161,6 +161,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     __syncwarp();
     if (ranks > 1) cluster_started();
+    // Tensor memory is this CTA's before any of its warps lets the next kernel be set up: that one
+    // may allocate before its own wait, and would hold what this one still waits for.
+    __syncthreads();
     follow_previous();
     build_groups<kThreads>(a, C::BN, offset, first_tile, warp_tiles);
     tc_fence_before_sync();

@@ -287,6 +287,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         abort_flag = 0;
         fence_mbar_init();
     }
+    __syncthreads();  // tensor memory is this CTA's before the next kernel may be set up and take it
     follow_previous();
     build_groups<kPairThreads>(a, kPairTokens, offset, first_tile, warp_tiles);
     tc_fence_before_sync();

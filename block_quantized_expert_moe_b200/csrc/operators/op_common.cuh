@@ -146,7 +146,8 @@ __device__ __forceinline__ float cluster_ld_f32(uint32_t addr)
 
 // Waits until everything before this kernel on the stream has finished and its memory is
 // visible, then lets the next kernel's blocks be set up (in this order: a follower that
-// reads weights before its own wait must not overtake what precedes this kernel).  Global
+// reads weights before its own wait must not overtake what precedes this kernel).  One thread's
+// call counts for its CTA: a CTA that allocates tensor memory has a barrier in between.  Global
 // memory is read with plain loads and through pointers that are not __restrict__: a read-only
 // load could be moved ahead of the wait, or hit a line cached before it.
 __device__ __forceinline__ void follow_previous()

@@ -43,3 +43,48 @@ def test_grouped_product_of_a_thousand_falling_offsets():
     out = before.clone()
     bq().moe_fp8_grouped_matmul(a, sa, b, sb, torch.from_numpy(offsets.astype(np.int32)).cuda(), out)
     check_groups(out, before, a, sa, b, sb, np.maximum.accumulate(np.clip(offsets, 0, R)), K)
+
+
+# ---- kernels that follow one another -------------------------------------------------------------
+
+def test_products_and_layer_forwards_in_a_row_share_tensor_memory():
+    """Every kernel here allocates tensor memory before it waits for the one before it, up to all of an SM's:
+    few-row products with and without a K split, pair products and the layer's one-launch tail in turn,
+    eager and captured, nothing waited for in between, give what the calls one by one give."""
+    import synth
+    from harness import router_to_device, to_device
+    m = bq()
+    wl = synth.WORKLOADS["tiny_q8"]
+    li = synth.layer_inputs(wl, 0)
+    pack = m.pack_layer(li, max_tokens=8)
+    x = to_device(synth.tokens(wl, li.router, 0, 0, 8))
+    wr = router_to_device(li.router)
+    y = torch.zeros(8, wl.hidden, device="cuda")
+    products = []
+    for R, N, K in ((1, 256, 512), (40, 512, 1024), (2000, 1000, 256), (4096, 1536, 384), (5, 20000, 130)):
+        a, sa, b, sb = operands(R, N, K, R)
+        products.append((a, sa, b, sb, torch.zeros(R, N, device="cuda")))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def sequence(wait):
+        for i in (0, 1, 2, 3, 4, 1, 3, 0, 3, 4, 0):
+            m.moe_fp8_matmul(*products[i], status)
+            wait()
+            if i != 4:
+                m.moe_layer_forward(x, wr, pack, m.MOE_FMT_FROM_PACK, wl.top_k, y)
+                wait()
+
+    outs = [p[-1] for p in products] + [y]
+    sequence(torch.cuda.synchronize)
+    want = [t.clone() for t in outs]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        sequence(lambda: None)
+    for run in [lambda: sequence(lambda: None)] * 5 + [g.replay] * 5:
+        for t in outs:
+            t.zero_()
+        run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert int(status) == 0 and m.moe_get_device_error(pack) == m.MOE_OK
+    pack.free()
