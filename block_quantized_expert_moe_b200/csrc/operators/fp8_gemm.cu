@@ -159,7 +159,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         abort_flag = 0;
         fence_mbar_init();
     }
-    __syncwarp();
     if (ranks > 1) cluster_started();
     // Tensor memory is this CTA's before any of its warps lets the next kernel be set up: that one
     // may allocate before its own wait, and would hold what this one still waits for.

@@ -94,21 +94,25 @@ __device__ __forceinline__ unsigned cluster_size()
     return r;
 }
 
+// (The .aligned forms take whole warps: lanes that come from a branch meet first.)
 __device__ __forceinline__ void cluster_sync()
 {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // A CTA's shared memory may be written by the others once it has started: each arrives when
-// it starts and waits before it sends.  (All threads of a converged warp; waits for residents of
-// one cluster, which are scheduled together.)
+// it starts and waits before it sends.  (It waits for residents of one cluster, which are
+// scheduled together.)
 __device__ __forceinline__ void cluster_started()
 {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void cluster_wait_started()
 {
+    __syncwarp();
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 

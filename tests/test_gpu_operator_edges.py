@@ -8,7 +8,7 @@ import op_reference as ref
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from test_gpu_operators import bq, check_groups, operands
+from test_gpu_operators import bq, check_balance, check_groups, check_product, operands
 
 
 # 40 rows (the kernel for few rows) and many rows of every group (the kernel of CTA pairs)
@@ -88,3 +88,29 @@ def test_products_and_layer_forwards_in_a_row_share_tensor_memory():
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
     assert int(status) == 0 and m.moe_get_device_error(pack) == m.MOE_OK
     pack.free()
+
+
+# ---- clusters: barriers behind branches of a lane or of a part of a warp ----------------------------
+
+@pytest.mark.parametrize("R,N,K", [(7, 33, 1100), (16, 1001, 1024), (40, 4001, 640), (50, 129, 4096), (3, 1, 2048),
+                                   (64, 2047, 260)])
+def test_split_products_whose_last_columns_part_a_warp(R, N, K):
+    """K split over 2, 4 and 8 CTAs, n not a multiple of a warp's 32 rows of weights."""
+    a, sa, b, sb = operands(R, N, K, R * N)
+    first = None
+    for _ in range(3):
+        out = torch.full((R, N), float("nan"), device="cuda")
+        bq().moe_fp8_matmul(a, sa, b, sb, out)
+        check_product(out, a, sa, b, sb, K)
+        first = out if first is None else first
+        assert torch.equal(first, out)
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 33, 5), (17, 129, 3), (33, 200, 8), (100, 511, 10), (128, 1021, 7), (3000, 1021, 7)])
+def test_balance_loss_of_every_cluster_size_repeats(T, E, k):
+    g = torch.Generator(device="cuda").manual_seed(T + E)
+    logits = torch.randn(T, E, generator=g, device="cuda")
+    idx = logits.topk(k, 1).indices.int()
+    first = check_balance(logits, idx, None)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(first, check_balance(logits, idx, None)))
