@@ -260,7 +260,7 @@ __device__ void balance_reduce(const BalanceArgs &a, const float *s_sum, const i
 template <class T, int NV, int V, bool CLUSTER>
 __global__ void __launch_bounds__(kBalThreads, 1) balance_forward_kernel(const BalanceArgs a)
 {
-    extern __shared__ float bal_smem[];
+    extern __shared__ __align__(16) float bal_smem[];  // stored to 16 bytes at a time
     float *warp_cols = bal_smem;                                   // [kBalWarps][E]
     float *cta_sum = warp_cols + kBalWarps * a.E;                  // [E]
     int32_t *hist = reinterpret_cast<int32_t *>(cta_sum + a.E);    // [E]

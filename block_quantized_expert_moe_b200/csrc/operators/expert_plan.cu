@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     expert_plan_kernel(const int32_t *idx, int P, int k, int E, int bits, int warps, int32_t *counts,
                        int32_t *offsets, int32_t *rows, int32_t *slots)
 {
-    extern __shared__ int32_t smem[];
+    extern __shared__ __align__(16) int32_t smem[];  // cleared 16 bytes at a time
     int32_t *base = smem;                       // [E] first slot of this CTA's pairs of each expert
     int32_t *total = base + E;                  // [CTA of the cluster][E] pairs per expert, sent by each
     int32_t *hist = total + cluster_size() * E;  // [warps][E]

@@ -8,7 +8,7 @@ import op_reference as ref
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from test_gpu_operators import bq, check_balance, check_groups, check_product, operands
+from test_gpu_operators import bq, check_balance, check_groups, check_product, host, i32, operands
 
 
 # 40 rows (the kernel for few rows) and many rows of every group (the kernel of CTA pairs)
@@ -114,3 +114,19 @@ def test_balance_loss_of_every_cluster_size_repeats(T, E, k):
     first = check_balance(logits, idx, None)
     for _ in range(3):
         assert all(torch.equal(a, b) for a, b in zip(first, check_balance(logits, idx, None)))
+
+
+@pytest.mark.parametrize("T", [50, 700])
+@pytest.mark.parametrize("E", [3, 4, 7, 60, 1021, 1024])
+def test_plan_and_balance_loss_of_every_table_alignment(T, E):
+    """Tables in shared memory that start on 16 bytes (E a multiple of 4 or 8) and that do not."""
+    g = torch.Generator(device="cuda").manual_seed(E)
+    k = min(3, E)
+    for dt in (torch.float32, torch.bfloat16):
+        logits = torch.randn(T, E, generator=g, device="cuda").to(dt)
+        idx = logits.float().topk(k, 1).indices.int()
+        check_balance(logits, idx, None)
+    counts, offsets, rows, slots = i32(E), i32(E + 1), i32(T * k), i32(T, k)
+    bq().moe_expert_plan(idx, E, counts, offsets, rows, slots)
+    for got, want in zip((counts, offsets, rows, slots), ref.plan(host(idx), E)):
+        assert np.array_equal(host(got), want)
