@@ -70,13 +70,35 @@ __device__ __forceinline__ float amax8(const float (&v)[8])
 __device__ __forceinline__ float amax2(float a, float b) { return amax3(a, b, 0.f); }
 
 // g / (1 + exp(-g)) from the hardware's 2^t and reciprocal (2^-22 relative each); t = -g log2(e)
-// is rounded, which adds |g| 2^-24 for negative g.  A sigmoid below 2^-126 is 0.
+// is rounded, which adds |g| 2^-24 for negative g.  Down to kSiluFar the sigmoid is a normal number
+// (the reciprocal gives 0 for smaller ones).
+constexpr float kSiluFar = -87.f;
 __device__ __forceinline__ float silu(float g)
 {
     float e, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
     return g * r;
+}
+
+// Below kSiluFar, where 1 + exp(-g) rounds to exp(-g) and silu(g) is an fp32 number down to -104:
+// g exp(g) as (g h) h with h = exp(g / 2), which leaves the normal numbers in the last product only.
+__device__ __forceinline__ float silu_far(float g)
+{
+    const float h = expf(0.5f * g);
+    return (g * h) * h;
+}
+
+__device__ __forceinline__ float min3(float a, float b, float c)
+{
+    float m;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
+
+__device__ __forceinline__ float min8(const float (&v)[8], float m)
+{
+    return min3(min3(v[0], v[1], v[2]), min3(v[3], v[4], v[5]), min3(v[6], v[7], m));
 }
 
 // Eight values as loaded, and as fp32.
@@ -159,7 +181,7 @@ struct Kept {
 
 // The lane's eight columns of a block: 8 in a row, or for fp32 rows off 16-byte boundaries every
 // 16th, so that a load is consecutive.  (28,968 gathered rows of 1309: 36.1 us, 41.8 with 8 in a
-// row; for bf16 the codes' byte stores cost more: 60,000 SwiGLU rows of 513 46.4 us, 56.6 with
+// row; for bf16 the codes' byte stores cost more: 60,000 SwiGLU rows of 513 46.4 us then, 56.6 with
 // every 16th.)
 template <class T, bool WIDE>
 struct Columns {
@@ -168,9 +190,10 @@ struct Columns {
     static __device__ __forceinline__ int first(int b, int lane) { return b * kScaleBlock + lane * (SPREAD ? 1 : 8); }
 };
 
-// the lane's values of a block of a source row, or of its SwiGLU; zeros for no row
+// The lane's values of a block of a source row, or of its SwiGLU (WIDE: then `far` is set where a gate
+// is below kSiluFar, whose value is not right yet); zeros for no row.
 template <class T, bool SWIGLU, bool WIDE>
-__device__ __forceinline__ void row_values(const T *x, int b, int lane, int cols, float (&v)[8])
+__device__ __forceinline__ void row_values(const T *x, int b, int lane, int cols, float (&v)[8], bool &far)
 {
     const int c0 = Columns<T, WIDE>::first(b, lane);
 #pragma unroll
@@ -185,9 +208,53 @@ __device__ __forceinline__ void row_values(const T *x, int b, int lane, int cols
             const int c = c0 + j * Columns<T, WIDE>::STEP;
             w[j] = x && c < cols ? as_float(x[cols + c]) : 0.f;
         }
+        const bool some_far = min8(v, 0.f) < kSiluFar;
+        if (!WIDE && some_far) {  // (out of line 60,000 rows of 513 in bf16 take 51.7 us, so 47.3)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = silu(v[j]) * w[j];
+            for (int j = 0; j < 8; ++j) v[j] = (v[j] < kSiluFar ? silu_far(v[j]) : silu(v[j])) * w[j];
+        } else {
+            far = far || some_far;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = silu(v[j]) * w[j];
+        }
     }
+}
+
+// Whether a lane's sixteen gates may hold one below kSiluFar.  bf16: such a gate's bits are, as an
+// unsigned number, at or above those of -87.5 (NaNs with a sign are too), two gates an instruction on
+// the words as loaded.
+__device__ __forceinline__ bool has_far(const Raw8<__nv_bfloat16> &a, const Raw8<__nv_bfloat16> &b)
+{
+    const uint32_t m = __vmaxu2(__vmaxu2(__vmaxu2(a.r.x, a.r.y), __vmaxu2(a.r.z, a.r.w)),
+                                __vmaxu2(__vmaxu2(b.r.x, b.r.y), __vmaxu2(b.r.z, b.r.w)));
+    return m >= 0xc2af0000u || (m << 16) >= 0xc2af0000u;
+}
+__device__ __forceinline__ bool has_far(const Raw8<float> &a, const Raw8<float> &b)
+{
+    float v[8], w[8];
+    a.values(v);
+    b.values(w);
+    return min8(v, min8(w, 0.f)) < kSiluFar;
+}
+
+// The lane's values of a block, read once more, where some gate is far: seldom, so out of line (in line,
+// or with fp32 minima for the test, the usual path gets 48 registers or another order of its loads:
+// 36.5 to 43.4 us for 81,920 x 512 in bf16, 34.1 so).
+struct Eight {
+    float v[8];
+};
+
+template <class T>
+__device__ __noinline__ Eight far_values(const T *x, int b, int lane, int cols)
+{
+    Eight r;
+#pragma unroll 1
+    for (int j = 0; j < 8; ++j) {
+        const int c = Columns<T, true>::first(b, lane) + j * Columns<T, true>::STEP;
+        const float g = x && c < cols ? as_float(x[c]) : 0.f, u = x && c < cols ? as_float(x[cols + c]) : 0.f;
+        r.v[j] = (g < kSiluFar ? silu_far(g) : silu(g)) * u;
+    }
+    return r;
 }
 
 template <class T, bool WIDE>
@@ -216,7 +283,8 @@ constexpr int kQuantPer = kQuantThreads / 16 / kQuantRows;  // half-warps on a r
 constexpr int kQuantTurn = 2 * kQuantPer;                   // blocks of a row a CTA takes at a time
 
 template <class T, bool SWIGLU, bool WIDE>
-__global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const QuantArgs a)
+__global__ void __launch_bounds__(kQuantThreads, SWIGLU && WIDE && sizeof(T) == 2 ? 6 : 0)
+    quantize_rows_kernel(const QuantArgs a)
 {
     const int half = threadIdx.x >> 4, lane = threadIdx.x & 15;
     const int row = blockIdx.x * kQuantRows + (half & (kQuantRows - 1));
@@ -229,6 +297,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const Quan
     for (int b0 = half / kQuantRows + blockIdx.y * kQuantTurn; b0 < a.blocks; b0 += kQuantTurn * gridDim.y) {
         const int b1 = b0 + kQuantPer;
         float v0[8], v1[8];
+        bool far = false;
         if (WIDE && (b1 + 1) * kScaleBlock <= a.cols) {
             Raw8<T> g0 = {}, g1 = {}, u0 = {}, u1 = {};
             if (x) {
@@ -243,6 +312,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const Quan
             g0.values(v0);
             g1.values(v1);
             if (SWIGLU) {
+                far = has_far(g0, g1);
                 float w0[8], w1[8];
                 u0.values(w0);
                 u1.values(w1);
@@ -253,8 +323,13 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const Quan
                 }
             }
         } else {
-            row_values<T, SWIGLU, WIDE>(x, b0, lane, a.cols, v0);
-            row_values<T, SWIGLU, WIDE>(x, b1, lane, a.cols, v1);
+            row_values<T, SWIGLU, WIDE>(x, b0, lane, a.cols, v0, far);
+            row_values<T, SWIGLU, WIDE>(x, b1, lane, a.cols, v1, far);
+        }
+        if (SWIGLU && WIDE && far) {
+            const Eight f0 = far_values<T>(x, b0, lane, a.cols), f1 = far_values<T>(x, b1, lane, a.cols);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v0[j] = f0.v[j], v1[j] = f1.v[j];
         }
         const bool second = lane & 8;
         const float m0 = amax8(v0), m1 = amax8(v1);

@@ -466,7 +466,9 @@ moe_status moe_balance_loss_backward(const void *logits, moe_dtype dtype, const 
  *   rows    device [n_rows] int32: source row of each output row (a value
  *           outside [0, n_src_rows) gives a row of zeros), or NULL: output row
  *           r is source row r (n_src_rows == n_rows)
- *   swiglu  0, or 1: the value is silu(x[c]) * x[cols + c], in fp32
+ *   swiglu  0, or 1: the value is silu(x[c]) * x[cols + c] in fp32, with
+ *           silu(g) = g / (1 + exp(-g)) as an fp32 number (subnormal below
+ *           g = -91.8, 0 from -109 on; NaN for g = -inf)
  *   codes   device [n_rows x cols] bytes, row stride ld_codes (a multiple of
  *           16), 16-byte aligned; bytes between cols and ld_codes are not
  *           written

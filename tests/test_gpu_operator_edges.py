@@ -8,7 +8,8 @@ import op_reference as ref
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from test_gpu_operators import bq, check_balance, check_groups, check_product, host, i32, operands
+from test_gpu_operators import (DTYPES, bq, check_balance, check_groups, check_product, host, i32, operands, run_quantize,
+                                values)
 
 
 # 40 rows (the kernel for few rows) and many rows of every group (the kernel of CTA pairs)
@@ -130,3 +131,38 @@ def test_plan_and_balance_loss_of_every_table_alignment(T, E):
     bq().moe_expert_plan(idx, E, counts, offsets, rows, slots)
     for got, want in zip((counts, offsets, rows, slots), ref.plan(host(idx), E)):
         assert np.array_equal(host(got), want)
+
+
+# ---- SwiGLU where the sigmoid is below the smallest normal number -------------------------------------
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("C", [512, 1024, 100, 513])
+@pytest.mark.parametrize("low,high", [(-92, -87), (-88, -86), (-104, -93), (-120, 4)])
+def test_quantize_swiglu_of_far_negative_gates(low, high, C, dt):
+    """silu(g) = g / (1 + exp(-g)) is an fp32 number down to g = -104, though 1 / (1 + exp(-g)) leaves the
+    normal ones at -87.3; a large up half brings it back into range.
+
+    Below -87 the kernel forms (g h) h with h = expf(g / 2) (g / 2 is exact): expf is within 2 ulp, 2^-22
+    relative, twice, and two products round (2^-24 each); the product's result may be subnormal, rounded
+    to 2^-150.  Above it g r(1 + e(g)) with 2^t within 2^-22 and t = -g log2(e) rounded (|t| 2^-24, times
+    ln 2, |t| <= 126: 88 2^-24), an addition (2^-24), the reciprocal within 2^-23, a product.  Times up: one
+    rounding more.  Together at most 96 * 2^-24 relative and 2^-150 |up|."""
+    R = 9
+    g = torch.Generator(device="cuda").manual_seed(C)
+    gate = (low + (high - low) * torch.rand(R, C, generator=g, device="cuda")).to(DTYPES[dt])
+    up = (torch.randn(R, C, generator=g, device="cuda") * 1e30).to(DTYPES[dt])
+    codes, scales = run_quantize(torch.cat([gate, up], 1), R, C, swiglu=True)
+    v, u = ref.swiglu(host(torch.cat([gate, up], 1))), np.abs(host(up))
+    err = np.abs(v) * 96 * 2.0 ** -24 + u * 2.0 ** -150
+    nb = -(-C // 128)
+    blocks = lambda x: np.pad(x, ((0, 0), (0, nb * 128 - C))).reshape(R, nb, 128).max(2)
+    floor = float(ref.FLOOR)
+    s = host(scales).T
+    amax, most = np.maximum(blocks(np.abs(v)), floor), np.maximum(blocks(np.abs(v) + err), floor)
+    least = np.maximum(blocks(np.maximum(np.abs(v) - err, 0)), floor)
+    assert np.all(s <= most / 448 * (1 + 2.0 ** -23)) and np.all(s >= least / 448 * (1 - 2.0 ** -23))
+    assert amax.min() > 1e3 * floor  # the values count
+    per = np.repeat(s, 128, 1)[:, :C]
+    # half an E4M3 step: 2^-4 of the value, or 2^-10 of the scale below the smallest normal code
+    tol = np.maximum((np.abs(v) + err) * 2.0 ** -4, per * 2.0 ** -10) * (1 + 1e-5) + 2 * err
+    assert np.all(np.abs(values(codes) * per - v) <= tol)
