@@ -18,6 +18,7 @@ _CODES = (torch.float8_e4m3fn, torch.uint8)
 _MASKS = (torch.bool, torch.uint8)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_INT_MAX = 2 ** 31 - 1  # sizes cross the ABI as C ints, which ctypes would wrap without a word
 _NOT_PLAIN = (AttributeError, KeyError, TypeError, ValueError)  # what the one expression raises on other arguments
 
 
@@ -85,6 +86,12 @@ def _code_rows(t, name, shape):
     return ld
 
 
+def _sizes(**sizes):
+    for name, n in sizes.items():
+        if not -_INT_MAX <= n <= _INT_MAX:
+            raise ValueError(f"{name} = {n}: a size must be below 2**31")
+
+
 def _off_device(names, tensors):
     device = tensors[0].get_device()
     for name, t in zip(names, tensors):
@@ -121,6 +128,7 @@ def _run(fn, names, tensors, args, stream):
 def _plan_checks(idx, n_experts, counts, offsets, rows, slots):
     T, k = shape = _shape(idx, "idx", 2)
     i32 = (_I32,)
+    _sizes(tokens=T, top_k=k, n_experts=n_experts)
     _tensor(idx, "idx", i32, shape)
     _tensor(counts, "counts", i32, (n_experts,))
     _tensor(offsets, "offsets", i32, (n_experts + 1,))
@@ -139,7 +147,7 @@ def moe_expert_plan(idx, n_experts, counts, offsets, rows, slots, stream=None):
     behind the last one in use), slots int32 [T, k] (each pair's slot or -1)."""
     try:
         T, k = shape = idx.shape
-        plain = (idx.dtype is _I32 and counts.dtype is _I32 and offsets.dtype is _I32 and rows.dtype is _I32
+        plain = (T | k | n_experts <= _INT_MAX and idx.dtype is _I32 and counts.dtype is _I32 and offsets.dtype is _I32 and rows.dtype is _I32
                  and slots.dtype is _I32 and slots.shape == shape and counts.shape == (n_experts,)
                  and offsets.shape == (n_experts + 1,) and rows.shape == (T * k,) and idx.is_contiguous()
                  and slots.is_contiguous() and counts.is_contiguous() and offsets.is_contiguous()
@@ -154,12 +162,14 @@ def moe_expert_plan(idx, n_experts, counts, offsets, rows, slots, stream=None):
 
 
 def moe_balance_loss_workspace_bytes(n_tokens, n_experts):
+    _sizes(n_tokens=n_tokens, n_experts=n_experts)
     return lib.moe_balance_loss_workspace_bytes(n_tokens, n_experts)
 
 
 def _loss_checks(logits, idx, counts, prob_mean, loss, workspace, valid):
     T, E = shape = _shape(logits, "logits", 2)
     k = _shape(idx, "idx", 2)[1]
+    _sizes(tokens=T, experts=E, top_k=k)
     dt = _float_code(logits, "logits")
     _tensor(logits, "logits", (logits.dtype,), shape)
     _tensor(idx, "idx", (_I32,), (T, k))
@@ -186,7 +196,7 @@ def moe_balance_loss(logits, idx, counts, prob_mean, loss, workspace=None, valid
         T, E = logits.shape
         rows, k = idx.shape
         dt = _FLOAT_CODE[logits.dtype]
-        plain = (rows == T and idx.dtype is _I32 and counts.dtype is _I32 and prob_mean.dtype is _F32
+        plain = (rows == T and T | E | k <= _INT_MAX and idx.dtype is _I32 and counts.dtype is _I32 and prob_mean.dtype is _F32
                  and loss.dtype is _F32 and counts.shape == (E + 1,) and prob_mean.shape == (E,) and loss.shape == (1,)
                  and logits.is_contiguous() and idx.is_contiguous() and counts.is_contiguous()
                  and prob_mean.is_contiguous()
@@ -203,8 +213,9 @@ def moe_balance_loss(logits, idx, counts, prob_mean, loss, workspace=None, valid
           prob_mean.data_ptr(), ws, ws_bytes), stream)
 
 
-def _loss_backward_checks(logits, counts, dloss, dlogits, valid):
+def _loss_backward_checks(logits, counts, top_k, dloss, dlogits, valid):
     T, E = shape = _shape(logits, "logits", 2)
+    _sizes(tokens=T, experts=E, top_k=top_k)
     dt = _float_code(logits, "logits")
     same = (logits.dtype,)
     _tensor(logits, "logits", same, shape)
@@ -225,14 +236,14 @@ def moe_balance_loss_backward(logits, counts, top_k, dloss, dlogits, valid=None,
     try:
         T, E = shape = logits.shape
         dt = _FLOAT_CODE[logits.dtype]
-        plain = (dlogits.dtype is logits.dtype and counts.dtype is _I32 and dloss.dtype is _F32
+        plain = (0 <= T | E | top_k <= _INT_MAX and dlogits.dtype is logits.dtype and counts.dtype is _I32 and dloss.dtype is _F32
                  and dlogits.shape == shape and counts.shape == (E + 1,) and dloss.shape == (1,)
                  and logits.is_contiguous() and dlogits.is_contiguous() and counts.is_contiguous()
                  and (valid is None or valid.dtype in _MASKS and valid.shape == (T,) and valid.is_contiguous()))
     except _NOT_PLAIN:
         plain = False
     if not plain:
-        T, E, dt = _loss_backward_checks(logits, counts, dloss, dlogits, valid)
+        T, E, dt = _loss_backward_checks(logits, counts, top_k, dloss, dlogits, valid)
     mask = None if valid is None else valid.data_ptr()
     _run(lib.moe_balance_loss_backward, _LOSS_BACKWARD, (logits, counts, dloss, dlogits, valid),
          (logits.data_ptr(), dt, counts.data_ptr(), mask, dloss.data_ptr(), T, E, top_k, dlogits.data_ptr()), stream)
@@ -241,6 +252,7 @@ def moe_balance_loss_backward(logits, counts, top_k, dloss, dlogits, valid=None,
 def _quantize_checks(x, codes, scales, rows, swiglu):
     S, W = x_shape = _shape(x, "x", 2)
     R, C = shape = _shape(codes, "codes", 2)
+    _sizes(source_rows=S, rows=R, columns=W)
     dt = _float_code(x, "x")
     if W != (2 * C if swiglu else C):
         raise ValueError(f"x must have {2 * C if swiglu else C} columns, not {W}")
@@ -267,7 +279,7 @@ def moe_fp8_quantize(x, codes, scales, rows=None, swiglu=False, stream=None):
         ld_c, one_c = codes.stride()
         ld_s, one_s = scales.stride()
         dt = _FLOAT_CODE[x.dtype]
-        plain = (W == (C + C if swiglu else C) and codes.dtype in _CODES and scales.dtype is _F32
+        plain = (W == (C + C if swiglu else C) and S | R | W <= _INT_MAX and codes.dtype in _CODES and scales.dtype is _F32
                  and scales.shape == ((C + 127) >> 7, R) and one_x == 1 and one_c == 1
                  and (one_s == 1 or R == 1) and ld_x >= W
                  and ld_c >= C and not ld_c & 15 and ld_s >= R
@@ -293,6 +305,7 @@ def moe_fp8_quantize_weight(w, codes, scales, stream=None):
     dt = _float_code(w, "w")
     N, K = shape[-2:]
     G = shape[0] if len(shape) == 3 else 1
+    _sizes(groups=G, rows=N, columns=K)
     ld_w = _rows(w, "w", (w.dtype,), shape)
     ld_c = _code_rows(codes, "codes", shape)
     _tensor(scales, "scales", (_F32,), tuple(shape[:-2]) + (-(-N // 128), -(-K // 128)))
@@ -305,6 +318,7 @@ def _product_checks(a, a_scale, b, b_scale, out, groups):
     R, K = a_shape = _shape(a, "a", 2)
     b_shape = _shape(b, "b", 2 if groups is None else 3)
     N = b_shape[-2]
+    _sizes(rows=R, n=N, k=K, groups=b_shape[0])
     dt = _float_code(out, "out")
     KB = -(-K // 128)
     ld_a, ld_b = _code_rows(a, "a", a_shape), _code_rows(b, "b", (*b_shape[:-1], K))
@@ -339,8 +353,8 @@ def moe_fp8_matmul(a, a_scale, b, b_scale, out, status=None, stream=None):
         ld_o, one_o = out.stride()
         dt = _FLOAT_CODE[out.dtype]
         KB = (K + 127) >> 7
-        plain = (cols == K and a.dtype in _CODES and b.dtype in _CODES and a_scale.dtype is _F32
-                 and b_scale.dtype is _F32 and a_scale.shape == (KB, R) and b_scale.shape == ((N + 127) >> 7, KB)
+        plain = (cols == K and R | N | K <= _INT_MAX and a.dtype in _CODES and b.dtype in _CODES
+                 and a_scale.dtype is _F32 and b_scale.dtype is _F32 and a_scale.shape == (KB, R) and b_scale.shape == ((N + 127) >> 7, KB)
                  and out.shape == (R, N) and one_a == 1 and one_b == 1 and (one_s == 1 or R == 1) and one_o == 1
                  and not (ld_a | ld_b) & 15 and ld_a >= K and ld_b >= K and ld_s >= R and ld_o >= N
                  and b_scale.is_contiguous())
@@ -369,8 +383,8 @@ def moe_fp8_grouped_matmul(a, a_scale, b, b_scale, offsets, out, status=None, st
         ld_o, one_o = out.stride()
         dt = _FLOAT_CODE[out.dtype]
         KB = (K + 127) >> 7
-        plain = (cols == K and a.dtype in _CODES and b.dtype in _CODES and a_scale.dtype is _F32
-                 and b_scale.dtype is _F32 and offsets.dtype is _I32 and a_scale.shape == (KB, R)
+        plain = (cols == K and R | N | K | G <= _INT_MAX and a.dtype in _CODES and b.dtype in _CODES
+                 and a_scale.dtype is _F32 and b_scale.dtype is _F32 and offsets.dtype is _I32 and a_scale.shape == (KB, R)
                  and b_scale.shape == (G, (N + 127) >> 7, KB) and offsets.shape == (G + 1,) and out.shape == (R, N)
                  and one_a == 1 and one_b == 1 and (one_s == 1 or R == 1) and one_o == 1 and not (ld_a | ld_b) & 15
                  and ld_a >= K and ld_b >= K and ld_s >= R and ld_o >= N and b_scale.is_contiguous()
