@@ -111,6 +111,8 @@ def _load():
     L.moe_fp8_quantize_weight.argtypes = [vp, i32, i64, i64, i32, i32, i32, vp, i64, i64, vp, vp]
     L.moe_fp8_matmul.restype = i32
     L.moe_fp8_matmul.argtypes = [vp, i64, vp, i64, i32, vp, i64, vp, i32, i32, vp, i32, i64, vp, vp]
+    L.moe_debug_fp8_stall_after.restype = i32
+    L.moe_debug_fp8_stall_after.argtypes = [i32]
     L.moe_fp8_grouped_matmul.restype = i32
     L.moe_fp8_grouped_matmul.argtypes = [vp, i64, vp, i64, i32, vp, i64, i64, vp, vp, i32, i32, i32, vp, i32, i64, vp,
                                          vp]
@@ -268,6 +270,12 @@ def moe_debug_wait_timeout(pack, stream=None):
 def moe_debug_fail_alloc_after(n):
     """Tests only: the (n+1)-th device allocation of moe_pack_experts from now fails once (-1: off)."""
     _check(lib.moe_debug_fail_alloc_after(n), "moe_debug_fail_alloc_after")
+
+
+def moe_debug_fp8_stall_after(blocks):
+    """Tests only: E4M3 products launched from now on stop loading after `blocks` blocks a CTA, so that
+    their bounded waits run out (-1: off)."""
+    _check(lib.moe_debug_fp8_stall_after(blocks), "moe_debug_fp8_stall_after")
 
 
 def moe_debug_act_quant_nvfp4(x, stream=None):

@@ -28,6 +28,7 @@ struct ProductArgs {
     void *out;
     int64_t ld_out;
     int32_t *status;
+    int stall_after;  // K blocks a CTA loads before its producer stops, as if a copy never came (INT_MAX: never)
 };
 
 struct Operands {

@@ -33,6 +33,10 @@
 // one token's ten experts (20 MB) 9.3 us, one row x 1024 x 2048 4.2 us (group table
 // 1.1 us when its offsets are cold, first tile 2 us, exchange 1 us).
 // Every mbarrier wait is bounded.
+#include <limits.h>
+
+#include <atomic>
+
 #include "fp8_common.cuh"
 
 namespace moe {
@@ -192,7 +196,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (warp == kEpiWarps) {  // ---- TMA producer
             const int boxes = (ncols + kBox - 1) / kBox;
             for (int kb = kb0; kb < kb1 && go; ++kb) {
-                go = __all_sync(0xffffffffu, bar_wait(smem_u32(empty) + 8 * ring.slot, ring.phase ^ 1));
+                go = issued < a.stall_after &&
+                     __all_sync(0xffffffffu, bar_wait(smem_u32(empty) + 8 * ring.slot, ring.phase ^ 1));
                 if (!go) break;
                 if (elect_one()) {
                     uint8_t *w_s = smem + ring.slot * C::STAGE_BYTES, *x_s = w_s + kABytes;
@@ -336,15 +341,17 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         }
     }
-    // after a timed-out wait: let copies and MMAs in flight land before memory is released
+    tc_fence_before_sync();
+    __syncthreads();  // every warp is through: a wait that ran out in any of them is known here
+    tc_fence_after_sync();
+    // after one: let copies and MMAs in flight land before memory is released
     if (abort_flag) {
         if (warp == kEpiWarps && lane == 0) drain_ring(full, C::STAGES, issued);
         if (warp == kEpiWarps + 1 && elect_one()) drain_mma(&drain_bar);
         if (threadIdx.x == 0 && a.status) atomicExch(a.status, (int)MOE_ERR_TIMEOUT);
+        __syncthreads();
     }
-    tc_fence_before_sync();
-    __syncthreads();
-    tc_fence_after_sync();
+    __syncwarp();
     if (warp == kEpiWarps + 1) tmem_dealloc(tmem, kBufs * C::BN);
 }
 
@@ -372,6 +379,7 @@ moe_status run_product(const Operands &o, const ProductArgs &a, moe_dtype out_dt
 }
 
 PerDevice g_product;
+std::atomic<int> g_stall_after{INT_MAX};  // tests only (moe_debug_fp8_stall_after)
 
 cudaError_t product_prepare()
 {
@@ -410,6 +418,7 @@ moe_status product(const uint8_t *a, int64_t ld_a, const float *a_scale, int64_t
     p.out = out;
     p.ld_out = ld_out;
     p.status = status;
+    p.stall_after = g_stall_after.load(std::memory_order_relaxed);
     int sms = 0;
     const moe_status st = g_product.get(&sms, product_prepare);
     if (st != MOE_OK) return st;
@@ -454,6 +463,13 @@ moe_status product(const uint8_t *a, int64_t ld_a, const float *a_scale, int64_t
 }  // namespace moe
 
 using namespace moe;
+
+extern "C" moe_status moe_debug_fp8_stall_after(int blocks)
+{
+    if (blocks < -1) return MOE_ERR_INVALID_ARG;
+    g_stall_after.store(blocks < 0 ? INT_MAX : blocks, std::memory_order_relaxed);
+    return MOE_OK;
+}
 
 extern "C" moe_status moe_fp8_matmul(const uint8_t *a, int64_t ld_a, const float *a_scale, int64_t ld_a_scale, int rows,
                                      const uint8_t *b, int64_t ld_b, const float *b_scale, int n, int k, void *out,

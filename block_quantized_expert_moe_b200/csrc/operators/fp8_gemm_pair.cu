@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     __shared__ uint32_t tmem_base;
     __shared__ int warp_tiles[kPairThreads / 32];
     __shared__ volatile int abort_flag;
+    __shared__ int blocks_issued;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *out_stage = smem + kPairStages * kPairStage;  // [warp][32][128]
     int *offset = reinterpret_cast<int *>(out_stage + kEpiWarps * kOutBytes);
@@ -319,7 +320,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 const int x0 = t.row0 + (int)rank * mine;
                 for (int kb = 0; kb < a.kblocks; ++kb, ++issued, r.next()) {
                     // the slot's previous use has been multiplied (a fresh slot passes)
-                    if (!__all_sync(0xffffffffu, bar_wait(empty_at + 8 * r.slot, r.phase ^ 1))) {
+                    if (issued >= a.stall_after ||
+                        !__all_sync(0xffffffffu, bar_wait(empty_at + 8 * r.slot, r.phase ^ 1))) {
                         go = false;
                         break;
                     }
@@ -334,9 +336,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     __syncwarp();
                 }
             }
-            if (!go) {
-                if (lane == 0) abort_flag = 1;
-                if (rank == 0 && lane == 0) drain_ring(full, kPairStages, issued);
+            if (lane == 0) {
+                blocks_issued = issued;
+                if (!go) abort_flag = 1;
             }
         } else if (warp == kMmaWarp) {  // ---- MMA issuer
             // the whole warp runs the loop and one lane issues: in a branch of one lane the
@@ -371,11 +373,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         __syncwarp();
                     }
                 }
-                if (!go && elect_one()) {
-                    abort_flag = 1;
-                    mma2_commit(smem_u32(&drain_bar));
-                    mbar_wait(&drain_bar, 0);
-                }
+                if (!go && elect_one()) abort_flag = 1;
             }
         }
     } else {  // ---- epilogue
@@ -471,9 +469,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (WIDE && lane == 0) stores_done();
     }
     __syncwarp();
-    if (abort_flag && threadIdx.x == 0 && a.status) atomicExch(a.status, (int)MOE_ERR_TIMEOUT);
     tc_fence_before_sync();
-    __syncthreads();
+    __syncthreads();  // every warp is through: a wait that ran out in any of them is known here
+    // after one: let copies (of both CTAs, on the leader's barriers) and MMAs in flight land
+    if (abort_flag) {
+        if (rank == 0 && warp == kTmaWarp && lane == 0) drain_ring(full, kPairStages, blocks_issued);
+        if (rank == 0 && warp == kMmaWarp && elect_one()) {
+            mma2_commit(smem_u32(&drain_bar));
+            mbar_wait(&drain_bar, 0);
+        }
+        if (threadIdx.x == 0 && a.status) atomicExch(a.status, (int)MOE_ERR_TIMEOUT);
+    }
     cluster_sync();  // neither CTA leaves while the other may still arrive here or read its operands
     tc_fence_after_sync();
     if (warp == kMmaWarp) tmem_dealloc2(tmem, kPairBufs * kPairWeights);

@@ -337,6 +337,15 @@ moe_status moe_debug_fail_alloc_after(int n);
  * launch errors as the forward. */
 moe_status moe_debug_wait_timeout(const moe_pack *pack, void *stream);
 
+/* Fault injection for tests of the E4M3 products' failure path: in products
+ * launched after this call a CTA loads its first `blocks` (>= 0) blocks of 128
+ * columns and then no more, as if a copy never came; the kernel's bounded waits
+ * run out after about a second, what is in flight lands, and MOE_ERR_TIMEOUT is
+ * recorded.  A CTA that has no more blocks than that finishes.  -1 turns the
+ * injection off; less is MOE_ERR_INVALID_ARG.  Process-wide; no device is
+ * touched by this call. */
+moe_status moe_debug_fp8_stall_after(int blocks);
+
 /* Diagnostic for tests of the NVFP4 tensor-core prefill's activation rounding
  * (its reading of the block-scaled FP4 MMA, which needs both operands in NVFP4):
  * runs the prefill's own quantiser on `rows` plain rows and writes what it

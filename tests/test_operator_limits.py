@@ -52,3 +52,9 @@ CASES = {
 def test_binding_refuses_sizes_that_a_c_int_would_wrap(case):
     with pytest.raises(ValueError, match=r"2\*\*31"):
         CASES[case]()
+
+
+def test_stall_injection_refuses_other_negative_numbers():
+    with pytest.raises(bq.MoeError):
+        bq.moe_debug_fp8_stall_after(-2)
+    bq.moe_debug_fp8_stall_after(-1)
