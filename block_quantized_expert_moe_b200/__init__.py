@@ -111,6 +111,8 @@ def _load():
     L.moe_fp8_quantize_weight.argtypes = [vp, i32, i64, i64, i32, i32, i32, vp, i64, i64, vp, vp]
     L.moe_fp8_matmul.restype = i32
     L.moe_fp8_matmul.argtypes = [vp, i64, vp, i64, i32, vp, i64, vp, i32, i32, vp, i32, i64, vp, vp]
+    L.moe_fp8_get_device_error.restype = i32
+    L.moe_fp8_get_device_error.argtypes = []
     L.moe_debug_fp8_stall_after.restype = i32
     L.moe_debug_fp8_stall_after.argtypes = [i32]
     L.moe_fp8_grouped_matmul.restype = i32
@@ -446,7 +448,8 @@ def pack_layer(li, max_tokens=64, max_top_k=None, device=0, flags=0, expert_wind
 # The operators beside the layer (operators.py) are part of this namespace; they
 # need torch at import, which the rest of the package does not.
 _OPERATORS = ("moe_expert_plan", "moe_balance_loss_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward",
-              "moe_fp8_quantize", "moe_fp8_quantize_weight", "moe_fp8_matmul", "moe_fp8_grouped_matmul")
+              "moe_fp8_quantize", "moe_fp8_quantize_weight", "moe_fp8_matmul", "moe_fp8_grouped_matmul",
+              "moe_fp8_get_device_error")
 
 
 def __getattr__(name):

@@ -37,6 +37,26 @@ struct Operands {
     int k;
 };
 
+// Sticky error of the products of a source file on a device (a word for each file: device code is not
+// linked across them).
+namespace {
+__device__ int32_t device_error;
+
+__device__ __forceinline__ void record_timeout(int32_t *status)
+{
+    atomicExch(&device_error, (int)MOE_ERR_TIMEOUT);
+    if (status) atomicExch(status, (int)MOE_ERR_TIMEOUT);
+}
+
+// reads and clears the current device's word
+inline cudaError_t take_error(int32_t *error)
+{
+    const int32_t none = 0;
+    const cudaError_t e = cudaMemcpyFromSymbol(error, device_error, sizeof none);
+    return e != cudaSuccess || *error == 0 ? e : cudaMemcpyToSymbol(device_error, &none, sizeof none);
+}
+}  // namespace
+
 // kind::f8f6f4 instruction descriptor: E4M3 x E4M3 -> f32, both K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N)
 {
@@ -244,6 +264,7 @@ inline bool code_map(CUtensorMap *m, const void *base, int cols, int64_t rows, i
 // The pair kernel (fp8_gemm_pair.cu): two CTAs share a 256-row weight tile.
 constexpr int kPairTokens = 256;
 cudaError_t pair_prepare();
+cudaError_t pair_take_error(int32_t *error);
 moe_status pair_product(const Operands &o, const ProductArgs &a, moe_dtype out_dtype, int pairs, cudaStream_t s);
 
 }  // namespace fp8

@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (abort_flag) {
         if (warp == kEpiWarps && lane == 0) drain_ring(full, C::STAGES, issued);
         if (warp == kEpiWarps + 1 && elect_one()) drain_mma(&drain_bar);
-        if (threadIdx.x == 0 && a.status) atomicExch(a.status, (int)MOE_ERR_TIMEOUT);
+        if (threadIdx.x == 0) record_timeout(a.status);
         __syncthreads();
     }
     __syncwarp();
@@ -463,6 +463,17 @@ moe_status product(const uint8_t *a, int64_t ld_a, const float *a_scale, int64_t
 }  // namespace moe
 
 using namespace moe;
+
+extern "C" moe_status moe_fp8_get_device_error(void)
+{
+    int32_t few = 0, pair = 0;
+    if (cudaDeviceSynchronize() != cudaSuccess || take_error(&few) != cudaSuccess ||
+        pair_take_error(&pair) != cudaSuccess) {
+        cudaGetLastError();  // reported here, not by a later call
+        return MOE_ERR_CUDA;
+    }
+    return (moe_status)(few ? few : pair);
+}
 
 extern "C" moe_status moe_debug_fp8_stall_after(int blocks)
 {

@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             mma2_commit(smem_u32(&drain_bar));
             mbar_wait(&drain_bar, 0);
         }
-        if (threadIdx.x == 0 && a.status) atomicExch(a.status, (int)MOE_ERR_TIMEOUT);
+        if (threadIdx.x == 0) record_timeout(a.status);
     }
     cluster_sync();  // neither CTA leaves while the other may still arrive here or read its operands
     tc_fence_after_sync();
@@ -518,6 +518,8 @@ cudaError_t pair_prepare()
     if (e == cudaSuccess) e = cudaFuncSetAttribute(fp8_pair_kernel<__nv_bfloat16, false>, smem, kPairSmem);
     return e;
 }
+
+cudaError_t pair_take_error(int32_t *error) { return take_error(error); }
 
 moe_status pair_product(const Operands &o, const ProductArgs &a, moe_dtype out_dtype, int pairs, cudaStream_t s)
 {

@@ -10,7 +10,7 @@ stream.
 """
 import torch
 
-from . import MOE_DT_BF16, MOE_DT_F32, MOE_OK, MoeError, lib
+from . import MOE_DT_BF16, MOE_DT_F32, MOE_ERR_TIMEOUT, MOE_OK, MoeError, lib
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _FLOAT_CODE = {_F32: MOE_DT_F32, _BF16: MOE_DT_BF16}
@@ -343,7 +343,8 @@ def moe_fp8_matmul(a, a_scale, b, b_scale, out, status=None, stream=None):
     """out [R, N] (CUDA float32/bfloat16) = (a with a_scale) (b with b_scale)^T: a [R, K]
     and b [N, K] E4M3 codes (float8_e4m3fn or uint8, rows on multiples of 16 bytes),
     a_scale float32 [ceil(K / 128), R], b_scale float32 [ceil(N / 128), ceil(K / 128)].
-    status: int32 [1] that takes MOE_ERR_TIMEOUT if a device-side wait runs out."""
+    status: int32 [1] that takes MOE_ERR_TIMEOUT if a device-side wait runs out; without one only
+    moe_fp8_get_device_error tells."""
     try:
         R, K = a.shape
         N, cols = b.shape
@@ -373,7 +374,8 @@ _GROUPED = ("a", "a_scale", "b", "b_scale", "offsets", "out", "status")
 def moe_fp8_grouped_matmul(a, a_scale, b, b_scale, offsets, out, status=None, stream=None):
     """The product of moe_fp8_matmul per expert: rows [offsets[g], offsets[g + 1]) of a by
     matrix g of b [G, N, K] (b_scale [G, ceil(N / 128), ceil(K / 128)]); offsets int32
-    [G + 1] as moe_expert_plan writes them.  Rows outside every group keep their out."""
+    [G + 1] as moe_expert_plan writes them.  Rows outside every group keep their out.
+    status as moe_fp8_matmul's."""
     try:
         R, K = a.shape
         G, N, cols = b.shape
@@ -397,3 +399,14 @@ def moe_fp8_grouped_matmul(a, a_scale, b, b_scale, offsets, out, status=None, st
     _run(lib.moe_fp8_grouped_matmul, _GROUPED, (a, a_scale, b, b_scale, offsets, out, status),
          (a.data_ptr(), ld_a, a_scale.data_ptr(), ld_s, R, b.data_ptr(), ld_b, gs_b if G > 1 else 0, b_scale.data_ptr(),
           offsets.data_ptr(), G, N, K, out.data_ptr(), dt, ld_o, _status(status)), stream)
+
+
+def moe_fp8_get_device_error(device=None):
+    """MOE_ERR_TIMEOUT if a device-side wait of a product on `device` (None: the current one) has run out
+    since the last call, whose outputs are then undefined; else MOE_OK.  Waits for the device, then
+    clears the error."""
+    with torch.cuda.device(device):
+        status = lib.moe_fp8_get_device_error()
+    if status not in (MOE_OK, MOE_ERR_TIMEOUT):
+        raise MoeError(status, "moe_fp8_get_device_error")
+    return status

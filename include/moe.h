@@ -511,7 +511,8 @@ moe_status moe_fp8_quantize_weight(const void *w, moe_dtype w_dtype, int64_t ld_
  *   out      device [rows x n] fp32 or bf16, row stride ld_out elements
  *   status   device int32, or NULL: MOE_ERR_TIMEOUT is stored there if a
  *            bounded wait of the kernel runs out (outputs are then undefined);
- *            otherwise it is not written
+ *            otherwise it is not written.  With or without it the device's
+ *            error is set, which moe_fp8_get_device_error reads
  * a and b are 16-byte aligned and their row strides multiples of 16; n and k
  * are any sizes up to 2^20, rows up to 2^30.  rows == 0 enqueues nothing.  The
  * product by the transposed weights (the gradient of a) is the same call on the
@@ -534,6 +535,13 @@ moe_status moe_fp8_grouped_matmul(const uint8_t *a, int64_t ld_a, const float *a
                                   const uint8_t *b, int64_t ld_b, int64_t group_stride_b, const float *b_scale,
                                   const int32_t *offsets, int n_groups, int n, int k, void *out, moe_dtype out_dtype,
                                   int64_t ld_out, int32_t *status, void *stream);
+
+/* Sticky device-side error of the E4M3 products on the calling thread's current
+ * device: MOE_ERR_TIMEOUT if a bounded wait of any of them has run out since
+ * the last call (that product's outputs are undefined), whether or not it had a
+ * status word.  Synchronises the device, then clears the error.  Not during a
+ * capture. */
+moe_status moe_fp8_get_device_error(void);
 
 /* Sticky device-side error of the pack (synchronises its device), then clears it. */
 moe_status moe_get_device_error(const moe_pack *pack);

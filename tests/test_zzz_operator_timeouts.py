@@ -16,6 +16,7 @@ from test_gpu_operators import bq, check_product, operands
 def stall():
     yield bq().moe_debug_fp8_stall_after
     bq().moe_debug_fp8_stall_after(-1)
+    bq().moe_fp8_get_device_error()  # the next test finds none
 
 
 # one row and few rows, split over a cluster or not, one and several tiles a CTA; CTA pairs
@@ -66,3 +67,27 @@ def test_grouped_products_in_a_row_behind_one_whose_wait_ran_out(stall):
         torch.cuda.synchronize()
         assert int(status) == m.MOE_ERR_TIMEOUT and int(clean) == 0
         assert all(torch.equal(c[-1], w) for c, w in zip(calls, want))
+
+
+@pytest.mark.parametrize("R,N,K", [(1, 1024, 4096), (2000, 1000, 640)])
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_wait_that_ran_out_is_known_without_a_status_word(stall, R, N, K, captured):
+    m = bq()
+    a, sa, b, sb = operands(R, N, K, R)
+    out = torch.zeros(R, N, device="cuda")
+    m.moe_fp8_matmul(a, sa, b, sb, out)
+    assert m.moe_fp8_get_device_error() == m.MOE_OK
+    stall(1)
+    if captured:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            m.moe_fp8_matmul(a, sa, b, sb, out)
+        stall(-1)
+        g.replay()
+    else:
+        m.moe_fp8_matmul(a, sa, b, sb, out)
+        stall(-1)
+    m.moe_fp8_matmul(a, sa, b, sb, out)  # right, and does not clear the error
+    assert m.moe_fp8_get_device_error() == m.MOE_ERR_TIMEOUT
+    assert m.moe_fp8_get_device_error(0) == m.MOE_OK
+    check_product(out[-40:], a[-40:], sa[:, -40:], b, sb, K)
