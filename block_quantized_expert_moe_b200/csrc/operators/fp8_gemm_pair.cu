@@ -247,10 +247,10 @@ __device__ __forceinline__ void store_rows_anywhere(OUT *out, int64_t ld, uint32
     }
 }
 
-// The tile's token rows are split evenly between the CTAs; its columns (tcgen05 N) are a
-// multiple of 16.
+// The tile's token rows are split evenly between the CTAs, and so are its columns (tcgen05 N): a
+// multiple of 32, so that each CTA brings whole steps of 16 as a single one's instruction takes them.
 __device__ __forceinline__ int cta_rows(int rows) { return (rows + 1) / 2; }
-__device__ __forceinline__ int tile_columns(int left) { return left >= kPairWeights ? kPairWeights : (left + 15) & ~15; }
+__device__ __forceinline__ int tile_columns(int left) { return left >= kPairWeights ? kPairWeights : (left + 31) & ~31; }
 
 // WIDE: output rows start on 16-byte boundaries (map_y is then a map of the output).
 template <class OUT, bool WIDE>

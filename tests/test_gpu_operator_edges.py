@@ -166,3 +166,18 @@ def test_quantize_swiglu_of_far_negative_gates(low, high, C, dt):
     # half an E4M3 step: 2^-4 of the value, or 2^-10 of the scale below the smallest normal code
     tol = np.maximum((np.abs(v) + err) * 2.0 ** -4, per * 2.0 ** -10) * (1 + 1e-5) + 2 * err
     assert np.all(np.abs(values(codes) * per - v) <= tol)
+
+
+# ---- the last tile of columns of the CTA pairs ---------------------------------------------------------
+
+@pytest.mark.parametrize("left", [1, 15, 16, 17, 31, 32, 33, 48, 144, 240, 241])
+def test_pair_products_of_every_last_column_step(left):
+    """n just above a multiple of the 256 columns of a tile: the last tile's columns are split over both CTAs."""
+    R, N, K = 4000, 512 + left, 640
+    a, sa, b, sb = operands(R, N, K, left)
+    for dt in DTYPES.values():
+        out = torch.full((R, N + 7), -9.0, dtype=dt, device="cuda")
+        bq().moe_fp8_matmul(a, sa, b, sb, out[:, :N])
+        rows = slice(R - 300, R)
+        check_product(out[rows, :N], a[rows], sa[:, rows], b, sb, K)
+        assert bool((out[:, N:] == -9.0).all()) and torch.isfinite(out).all()
