@@ -179,10 +179,26 @@ __device__ __forceinline__ uint4 pack16(const float *v, __nv_bfloat16)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The warp's columns of its 32 rows, all of them inside the tile, a box at a time.
+__device__ __forceinline__ void copy_from_shared(float *out, uint32_t at)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    *out = v;
+}
+
+__device__ __forceinline__ void copy_from_shared(__nv_bfloat16 *out, uint32_t at)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+    *out = __ushort_as_bfloat16(v);
+}
+
+// The warp's columns of its 32 rows, all of them inside the tile, a box at a time.  A TMA store ends
+// on 16 bytes, beyond the map's last column if that does not (513 columns of fp32 in a wider buffer:
+// three more of each row were written): such a box leaves value by value.
 template <class OUT>
 __device__ __forceinline__ void store_rows(const CUtensorMap *map, uint32_t stage, const float (&acc)[kPart], int row0,
-                                           int n0, int n)
+                                           int n0, int n, OUT *out, int64_t ld)
 {
     constexpr int per = 16 / sizeof(OUT), cols = 128 / sizeof(OUT);  // columns of 16 bytes, of a box
     int lane;  // volatile: addresses computed from it are not kept in registers over the block loop
@@ -200,7 +216,15 @@ __device__ __forceinline__ void store_rows(const CUtensorMap *map, uint32_t stag
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0 && n0 + c < n) tma_store_2d(map, stage, n0 + c, row0);
+        const int left = n - n0 - c;
+        if (left > 0 && left < cols && left % per) {
+            for (int r = 0; r < 32; ++r)
+                for (int j = lane; j < left; j += 32)
+                    copy_from_shared(out + r * ld + c + j,
+                                     stage + r * 128 + ((j / per ^ (r & 7)) << 4) + j % per * (int)sizeof(OUT));
+        } else if (lane == 0 && left > 0) {
+            tma_store_2d(map, stage, n0 + c, row0);
+        }
     }
 }
 
@@ -461,7 +485,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             if (!WIDE) {
                 if (out_rows > 0) store_rows_anywhere<OUT>(out, a.ld_out, stage, acc, min(out_rows, 32), a.n - out_col);
             } else if (out_rows >= 32) {
-                store_rows<OUT>(&map_y, stage, acc, out_row, out_col, a.n);
+                store_rows<OUT>(&map_y, stage, acc, out_row, out_col, a.n, out, a.ld_out);
             } else if (lane < out_rows) {
                 store_row<OUT>(out + lane * a.ld_out, acc, a.n - out_col);
             }

@@ -181,3 +181,20 @@ def test_pair_products_of_every_last_column_step(left):
         rows = slice(R - 300, R)
         check_product(out[rows, :N], a[rows], sa[:, rows], b, sb, K)
         assert bool((out[:, N:] == -9.0).all()) and torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [*range(505, 521), 255, 257, 383, 1027])
+def test_pair_products_end_at_their_last_column(N, dt):
+    """Rows on 16-byte boundaries in a wider buffer, n at every distance from one: nothing behind it is
+    written, in whole tiles of rows and in the last ones of a group."""
+    counts, K = [3000, 0, 700, 437], 640
+    R = sum(counts)
+    a, sa, b, sb = operands(R, N, K, N, len(counts))
+    wide = torch.randn(R, -(-N // 8) * 8 + 8, device="cuda").to(DTYPES[dt])
+    before = wide.clone()
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    bq().moe_fp8_grouped_matmul(a, sa, b, sb, torch.from_numpy(offsets.astype(np.int32)).cuda(), wide[:, :N])
+    assert torch.equal(wide[:, N:], before[:, N:])
+    last = slice(offsets[2], offsets[3])
+    check_product(wide[last, :N], a[last], sa[:, last], b[2], sb[2], K)
