@@ -198,3 +198,70 @@ def test_pair_products_end_at_their_last_column(N, dt):
     assert torch.equal(wide[:, N:], before[:, N:])
     last = slice(offsets[2], offsets[3])
     check_product(wide[last, :N], a[last], sa[:, last], b[2], sb[2], K)
+
+
+# ---- operators behind copies, fills and joined streams ---------------------------------------------------
+
+def test_operators_behind_joined_streams_copies_and_fills():
+    """Each operator waits for all that precedes it: inputs that a copy, a fill or another stream's kernel
+    has just written, eager and in a captured fork and join, replayed on changed inputs."""
+    m = bq()
+    R, N, K, E, k = 700, 512, 640, 32, 2
+    a, sa, b, sb = operands(R, N, K, 5, E)
+    x = torch.empty(R // k, K, device="cuda")
+    host_x = torch.empty(R // k, K).pin_memory()
+    idx = torch.empty(R // k, k, dtype=torch.int32, device="cuda")
+    counts, offsets, rows, slots = i32(E), i32(E + 1), i32(R), i32(R // k, k)
+    xq, xs = torch.empty(R, K, dtype=torch.uint8, device="cuda"), torch.empty(K // 128, R, device="cuda")
+    out, dense = torch.empty(R, N, device="cuda"), torch.empty(R, N, device="cuda")
+    side = torch.cuda.Stream()
+
+    def run():
+        main = torch.cuda.current_stream()
+        x.copy_(host_x, non_blocking=True)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):  # the plan and a product beside the copies
+            m.moe_expert_plan(idx, E, counts, offsets, rows, slots)
+            m.moe_fp8_matmul(a, sa, b[0], sb[0], dense)
+        out.zero_()
+        main.wait_stream(side)
+        m.moe_fp8_quantize(x, xq, xs, rows=rows)
+        m.moe_fp8_grouped_matmul(xq, xs, b, sb, offsets, out)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            dense.add_(out)
+        main.wait_stream(side)
+        m.moe_expert_plan(idx, E, counts, offsets, rows, slots)
+
+    def fill(s):
+        g = torch.Generator().manual_seed(s)
+        host_x.copy_(torch.randn(R // k, K, generator=g))
+        idx.copy_(torch.randint(0, E, (R // k, k), generator=g, dtype=torch.int32))
+
+    def want():
+        torch.cuda.synchronize()
+        m.moe_expert_plan(idx, E, counts, offsets, rows, slots)
+        torch.cuda.synchronize()
+        m.moe_fp8_quantize(host_x.cuda(), xq, xs, rows=rows)
+        torch.cuda.synchronize()
+        m.moe_fp8_grouped_matmul(xq, xs, b, sb, offsets, out)
+        m.moe_fp8_matmul(a, sa, b[0], sb[0], dense)
+        torch.cuda.synchronize()
+        dense.add_(out)
+        return out.clone(), dense.clone(), slots.clone()
+
+    fill(0)
+    want()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for s in range(1, 9):
+        fill(s)
+        expected = want()
+        for call in (run, g.replay):
+            for t in (x, out, dense, xs):
+                t.fill_(float("nan"))
+            xq.fill_(0x7F), rows.fill_(-1), offsets.fill_(0), slots.fill_(-5)
+            call()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip((out, dense, slots), expected))
