@@ -482,6 +482,7 @@ extern "C" moe_status moe_balance_loss(const void *logits, moe_dtype dtype, cons
                                        float *prob_mean, void *workspace, size_t workspace_bytes, void *stream)
 {
     if (!balance_sizes_ok(dtype, n_tokens, n_experts, top_k)) return MOE_ERR_INVALID_ARG;
+    if ((int64_t)n_tokens * top_k > INT32_MAX) return MOE_ERR_INVALID_ARG;  // one expert may have them all
     if (!loss || !counts || !prob_mean) return MOE_ERR_INVALID_ARG;
     if (n_tokens && (!logits || !idx)) return MOE_ERR_INVALID_ARG;
     if (!aligned(logits, dtype == MOE_DT_BF16 ? 2 : 4) || !aligned(idx, 4) || !aligned(loss, 4) ||

@@ -446,7 +446,8 @@ size_t moe_balance_loss_workspace_bytes(int n_tokens, int n_experts);
  *   workspace device, 16-byte aligned, moe_balance_loss_workspace_bytes bytes
  *             (NULL when that is 0); its contents need no initialisation.  Two
  *             calls that may run at the same time need one each.
- * 1 <= top_k <= n_experts <= 1024, n_tokens <= 2^30.  A logit of -inf has
+ * 1 <= top_k <= n_experts <= 1024, n_tokens <= 2^30, n_tokens * top_k < 2^31
+ * (a token may name an expert more than once).  A logit of -inf has
  * probability 0; a token whose logits are all -inf adds nothing to P; a NaN or
  * +inf makes its token's probabilities NaN.  With no token that counts, loss,
  * counts and P are 0.  Sums are fp32 in a fixed order: results are reproducible
@@ -514,7 +515,7 @@ moe_status moe_fp8_quantize_weight(const void *w, moe_dtype w_dtype, int64_t ld_
  *            otherwise it is not written.  With or without it the device's
  *            error is set, which moe_fp8_get_device_error reads
  * a and b are 16-byte aligned and their row strides multiples of 16; n and k
- * are any sizes up to 2^20, rows up to 2^30.  rows == 0 enqueues nothing.  The
+ * are any sizes from 1 to 2^20, rows up to 2^30.  rows == 0 enqueues nothing.  The
  * product by the transposed weights (the gradient of a) is the same call on the
  * transposed codes and block scales. */
 moe_status moe_fp8_matmul(const uint8_t *a, int64_t ld_a, const float *a_scale, int64_t ld_a_scale, int rows,

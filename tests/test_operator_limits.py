@@ -58,3 +58,10 @@ def test_stall_injection_refuses_other_negative_numbers():
     with pytest.raises(bq.MoeError):
         bq.moe_debug_fp8_stall_after(-2)
     bq.moe_debug_fp8_stall_after(-1)
+
+
+def test_balance_loss_refuses_more_choices_than_its_counts_hold():
+    """Counts are int32, and one expert may be named by every choice."""
+    from test_operators_abi import INVALID, call
+    assert call("moe_balance_loss", T=1 << 30, k=2, ws_bytes=1 << 16) == INVALID
+    assert call("moe_balance_loss", T=(1 << 28) + 1, k=8, ws_bytes=1 << 16) == INVALID
