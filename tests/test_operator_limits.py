@@ -65,3 +65,89 @@ def test_balance_loss_refuses_more_choices_than_its_counts_hold():
     from test_operators_abi import INVALID, call
     assert call("moe_balance_loss", T=1 << 30, k=2, ws_bytes=1 << 16) == INVALID
     assert call("moe_balance_loss", T=(1 << 28) + 1, k=8, ws_bytes=1 << 16) == INVALID
+
+
+# ---- every rule is written twice: in one expression, and as checks with their reasons ------------------
+
+def cpu(*shape, dtype=F32):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+def layouts():
+    """Calls that are right: contiguous, in wider buffers, of one row, one column, one group, no row."""
+    c = cpu
+    yield "plan", bq.moe_expert_plan, (c(3, 2, dtype=I32), 4, c(4, dtype=I32), c(5, dtype=I32), c(6, dtype=I32),
+                                       c(3, 2, dtype=I32))
+    yield "no tokens", bq.moe_expert_plan, (c(0, 2, dtype=I32), 4, c(4, dtype=I32), c(5, dtype=I32), c(0, dtype=I32),
+                                            c(0, 2, dtype=I32))
+    for dt in (F32, torch.bfloat16):
+        for valid in (None, c(3, dtype=torch.bool), c(3, dtype=U8)):
+            yield "loss", bq.moe_balance_loss, (c(3, 4, dtype=dt), c(3, 2, dtype=I32), c(5, dtype=I32), c(4), c(1),
+                                                c(64, dtype=U8), valid)
+            yield "gradient", bq.moe_balance_loss_backward, (c(3, 4, dtype=dt), c(5, dtype=I32), 2, c(1),
+                                                             c(3, 4, dtype=dt), valid)
+    for R, C in ((5, 32), (5, 130), (1, 33), (0, 32), (5, 1), (1, 1)):
+        codes, scales = c(R, -(-C // 16) * 16, dtype=U8)[:, :C], c(-(-C // 128), R + 3)[:, 2:R + 2]
+        yield "rows", bq.moe_fp8_quantize, (c(R, C), codes, scales)
+        yield "wider", bq.moe_fp8_quantize, (c(R, C + 5)[:, 3:C + 3], codes, scales)
+        yield "gather", bq.moe_fp8_quantize, (c(9, C), codes, scales, c(R, dtype=I32))
+        yield "swiglu", bq.moe_fp8_quantize, (c(R, 2 * C), codes, scales, None, True)
+    for R, N, K in ((5, 7, 32), (5, 200, 130), (1, 7, 32), (5, 1, 32), (5, 7, 1), (1, 1, 1), (0, 7, 32)):
+        kb, nb, w = -(-K // 128), -(-N // 128), -(-K // 16) * 16
+        a, sa, out = c(R, w + 16, dtype=U8)[:, :K], c(kb, R + 2)[:, :R], c(R, N + 3)[:, 1:N + 1]
+        b = c(N, w, dtype=U8)[:, :K].view(torch.float8_e4m3fn)
+        yield "product", bq.moe_fp8_matmul, (a, sa, b, c(nb, kb), out)
+        yield "status", bq.moe_fp8_matmul, (a, sa, b, c(nb, kb), c(R, N, dtype=torch.bfloat16), c(1, dtype=I32))
+        for G in (1, 3):
+            b = c(G, N, w, dtype=U8)[..., :K]
+            yield "groups", bq.moe_fp8_grouped_matmul, (a, sa, b, c(G, nb, kb), c(G + 1, dtype=I32), out)
+
+
+CALLS = [(f"{name}-{i}", fn, args) for i, (name, fn, args) in enumerate(layouts())]
+
+
+@pytest.fixture
+def recorded(monkeypatch):
+    """The arguments that reach the library, by the expression first or by the checks alone."""
+    from block_quantized_expert_moe_b200 import operators
+
+    def run(fn, args, checks):
+        calls = []
+        with monkeypatch.context() as m:
+            m.setattr(operators, "_run", lambda f, names, tensors, values, stream: calls.append((f, values)))
+            if checks:  # no size passes the expression
+                m.setattr(operators, "_INT_MAX", -1)
+                m.setattr(operators, "_sizes", lambda **sizes: None)
+            fn(*args)
+        return calls
+    return run
+
+
+# A stride that is never used (of one row, or of a single row of scales) may differ.
+UNUSED = {"moe_fp8_quantize": {2: lambda v: v[4] <= 1, 9: lambda v: v[5] <= 1, 11: lambda v: v[6] <= 128},
+          "moe_fp8_matmul": {1: lambda v: v[4] <= 1, 3: lambda v: v[9] <= 128, 6: lambda v: v[8] <= 1,
+                             12: lambda v: v[4] <= 1},
+          "moe_fp8_grouped_matmul": {1: lambda v: v[4] <= 1, 3: lambda v: v[12] <= 128, 6: lambda v: v[11] <= 1,
+                                     15: lambda v: v[4] <= 1}}
+
+
+@pytest.mark.parametrize("name,fn,args", CALLS, ids=[c[0] for c in CALLS])
+def test_the_expression_and_the_checks_pass_the_same_arguments(recorded, name, fn, args):
+    (f, fast), = recorded(fn, args, False)
+    (g, slow), = recorded(fn, args, True)
+    assert f is g and len(fast) == len(slow)
+    unused = UNUSED.get(f.__name__, {})
+    for i, (x, y) in enumerate(zip(fast, slow)):
+        assert x == y or (i in unused and unused[i](fast)), (i, fast, slow)
+
+
+def test_the_checks_alone_refuse_what_the_binding_refuses(recorded):
+    """The refusals of test_operators_abi, without the expression before them."""
+    import test_operators_abi as abi
+    params = next(m for m in abi.test_binding_refuses_bad_tensors.pytestmark if m.name == "parametrize").args[1]
+    for case, over, error, match in params:
+        if match == "CUDA" or "status" in over:
+            continue  # refused behind the checks
+        fn, args = abi.CASES[case]
+        with pytest.raises(error, match=match):
+            recorded(lambda: fn(**{**args, **over}), (), True)
