@@ -438,13 +438,16 @@ moe_status product(const uint8_t *a, int64_t ld_a, const float *a_scale, int64_t
     int ranks = 1;
     while (ranks < 8 && narrow * ranks * 2 <= (token ? slots : sms) && ranks * 2 <= p.kblocks) ranks *= 2;
     // The pair kernel, or this one.  Many waves of tiles: by the rows a group has on average, since
-    // both read every weight once (128 experts of 1024 x 2048, pair against narrow: 32 rows 73.1 /
-    // 59.9 us, 48 rows 74.8 / 68.0, 64 rows 76.4 / 76.7, 128 rows 88.4 / 123.7; 512 experts of 2048 x
-    // 512, 40 rows 188 / 168).  Few waves: by the blocks that the busiest CTA takes one after another,
-    // 0.5 us each for a pair, 0.65 us for a narrow tile alone on its SM and 0.9 us for two, and 1 us for
-    // a cluster's exchange (rows x n x k, pair / narrow: 128 x 4096 x 4096 17.8 / 15.7 us, 256 x 4096 x
-    // 4096 18.9 / 22.8, 1024 x 4096 x 4096 20.5 / 54.5, 256 x 1024 x 2048 12.1 / 8.9, 1024 x 1024 x 1024
-    // 9.1 / 10.3, 4096 x 512 x 512 7.6 / 10.4; 8 experts of 2048 x 2048, 64 rows 14.5 / 18.2).
+    // both read every weight once (128 experts of 1024 x 2048, pair against narrow: 32 rows 67.0 /
+    // 58.7 us, 48 rows 68.8 / 67.9, 64 rows 69.9 / 80.3, 128 rows 81.3 / 132.7; 512 experts of 2048 x
+    // 512: 40 rows 162 / 170 to 181, 160 rows 224 / 458).  Few waves: by the blocks that the busiest CTA
+    // takes one after another, 0.5 us each for a pair, 0.65 us for a narrow tile alone on its SM and
+    // 0.9 us for two, and 1 us for a cluster's exchange (fitted when that read the others' sums; it
+    // costs less since, which turns none of these; rows x n x k, pair / narrow: 64 x 4096 x 4096
+    // 16.6 / 9.2 us, 128 x 4096 x 4096 17.1 / 13.2, 256 x 4096 x 4096 18.4 / 20.8, 512 x 4096 x 4096
+    // 18.8 / 26.5, 1024 x 4096 x 4096 19.7 / 50.1, 256 x 1024 x 2048 11.5 / 7.4, 333 x 1000 x 1111
+    // 8.8 / 7.5, 512 x 1024 x 1024 8.5 / 7.1, 1024 x 1024 x 1024 8.5 / 9.2, 4096 x 512 x 512 7.0 / 8.5;
+    // 8 experts of 2048 x 2048, 64 rows 14.2 / 18.8).
     bool pair = !token;
     if (wide >= 4 * pairs) {
         pair = pair && (int64_t)rows > 56ll * groups;

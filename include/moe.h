@@ -409,8 +409,8 @@ moe_status moe_debug_tail_plan(int n_tokens, int max_tokens, int hidden, int n_e
  * All of them only enqueue on `stream`: no allocation, no host
  * synchronisation, capturable.  Pointers are device memory of the calling
  * thread's current device and are aligned to their element unless an entry
- * says otherwise.  Nothing is kept from one call for the next.  Outputs do not
- * overlap inputs. */
+ * says otherwise.  Nothing is kept from one call for the next but the products'
+ * sticky error (moe_fp8_get_device_error).  Outputs do not overlap inputs. */
 
 /* Pairs sorted by expert.  Pair p = t * top_k + j is choice j of token t.
  *   idx      device [n_tokens x top_k] int32 (as moe_route_topk writes it); a
